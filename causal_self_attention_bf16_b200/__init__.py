@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -49,6 +49,11 @@ SIGNATURES = {
     "attn_decode_ex": ([_VP] * 7 + [_SZ] + [_I] * 6 + [_F, _I, _VP], _I),
     "attn_qk_norm_rope": ([_VP] * 5 + [_I] * 5 + [_F, _F, _I, _VP], _I),
     "attn_qk_norm_rope_bwd": ([_VP] * 7 + [_I] * 5 + [_F, _F, _I, _VP], _I),
+    "attn_kvq_write": ([_VP] * 7 + [_I] * 7 + [_VP], _I),
+    "attn_kvq_read": ([_VP] * 7 + [_I] * 7 + [_VP], _I),
+    "attn_decode_kvq_workspace_bytes": ([_I] * 6, _SZ),
+    "attn_decode_kvq_kernels": ([_I] * 7, _I),
+    "attn_decode_kvq": ([_VP] * 9 + [_SZ] + [_I] * 8 + [_F, _I, _VP], _I),
     "attn_get_device_error": ([ctypes.POINTER(ctypes.c_uint32)], _I),
     "attn_clear_device_error": ([], _I),
     "attn_set_wait_limit_ns": ([_U64], _I),
@@ -333,6 +338,148 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, c
     return o, lse
 
 
+class KVQCache(NamedTuple):
+    """A quantised key/value cache for B sequences, H_kv heads and room for Tk positions: per head vector, `bits`-bit
+    codes (4 or 8) and a bf16 (scale, zero) pair per group of `group` dims (32, 64 or 128); a code n stands for
+    n * scale + zero. Codes are uint8 [B, H_kv, Tk, 128 * bits // 8] (4 bits: the even dim in the low half of its
+    byte), params bf16 [B, H_kv, Tk, 128 // group, 2]. The functions below take any 4-tuple of such tensors."""
+
+    k_codes: torch.Tensor
+    k_params: torch.Tensor
+    v_codes: torch.Tensor
+    v_params: torch.Tensor
+
+    @property
+    def bits(self) -> int:
+        return self.k_codes.shape[3] * 8 // 128
+
+    @property
+    def group(self) -> int:
+        return 128 // self.k_params.shape[3]
+
+
+def kvq_cache(B: int, H_kv: int, Tk: int, bits: int = 4, group: int = 64, device="cuda", D: int = 128) -> KVQCache:
+    """An empty (zero) quantised cache."""
+    if min(B, H_kv, Tk) < 1:
+        raise ValueError("B, H_kv and Tk must be >= 1")
+    if bits not in (4, 8) or group not in (32, 64, 128) or D != 128:
+        raise ValueError("the cache is held in 4 or 8 bits, in groups of 32, 64 or 128 of D = 128 dims")
+    codes, params = (B, H_kv, Tk, D * bits // 8), (B, H_kv, Tk, D // group, 2)
+    return KVQCache(*(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)
+                      for shape, dtype in ((codes, torch.uint8), (params, torch.bfloat16))))
+
+
+def _check_kvq(cache):
+    """Check the cache's four tensors (all on one device). Returns (their pointers, B, H_kv, Tk, bits, group,
+    device)."""
+    if not isinstance(cache, (tuple, list)) or len(cache) != 4 or not all(isinstance(t, torch.Tensor) for t in cache):
+        raise ValueError("cache must be a KVQCache or a tuple (k_codes, k_params, v_codes, v_params)")
+    kc, kp, vc, vp = cache
+    dev, cs, ps = kc.device, kc.shape, kp.shape
+    if len(cs) != 4 or cs[3] not in (64, 128) or min(cs) < 1:
+        raise ValueError(f"k_codes has shape {tuple(cs)}; expected [B, H_kv, Tk, 64] (4 bits) or [.., 128] (8 bits)")
+    if len(ps) != 5 or ps[:3] != cs[:3] or ps[3] not in (1, 2, 4) or ps[4] != 2:
+        raise ValueError(f"k_params has shape {tuple(ps)}; expected [{cs[0]}, {cs[1]}, {cs[2]}, 128 // group, 2]")
+    for name, t, shape, dtype in (("k_codes", kc, cs, torch.uint8), ("k_params", kp, ps, torch.bfloat16),
+                                  ("v_codes", vc, cs, torch.uint8), ("v_params", vp, ps, torch.bfloat16)):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}; every tensor of one call must be on {dev}")
+    return (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), cs[0], cs[1], cs[2], cs[3] // 16, 128 // ps[3], dev
+
+
+def _check_seqlens(cache_seqlens, B: int, dev: torch.device):
+    if (not isinstance(cache_seqlens, torch.Tensor) or cache_seqlens.dtype != torch.int32 or
+            tuple(cache_seqlens.shape) != (B,) or cache_seqlens.device != dev or not cache_seqlens.is_contiguous()):
+        raise ValueError("cache_seqlens must be a contiguous int32 [B] tensor on the cache's device")
+
+
+def kvq_write(cache, k: torch.Tensor, v: torch.Tensor, cache_seqlens: torch.Tensor,
+              stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantise the T newest tokens' keys and values, bf16 [B, T, H_kv, D], into the cache (KVQCache) in place.
+    cache_seqlens: int32 [B] on the device, the valid keys of each sequence, the new tokens included: token i of
+    sequence b is written at position cache_seqlens[b] - T + i, or not at all where that is below 0."""
+    lib = load_library()
+    ptrs, B, Hkv, Tk, bits, group, dev = _check_kvq(cache)
+    _require_cuda("k_codes", cache[0])
+    _check_qkv("k", k, device=dev)
+    T, D = k.shape[1], k.shape[3]
+    if (k.shape[0], k.shape[2]) != (B, Hkv):
+        raise ValueError(f"k has shape {tuple(k.shape)}; expected [{B}, T, {Hkv}, {D}]")
+    _check_qkv("v", v, k.shape, dev)
+    _check_seqlens(cache_seqlens, B, dev)
+    with torch.cuda.device(dev):
+        st = lib.attn_kvq_write(k.data_ptr(), v.data_ptr(), *ptrs, cache_seqlens.data_ptr(), B, T, Hkv, Tk, D, bits,
+                                group, _stream_handle(stream, dev))
+    _check("attn_kvq_write", st)
+
+
+def kvq_read(cache, T: Optional[int] = None, cache_seqlens: Optional[torch.Tensor] = None,
+             k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Read keys and values back from the cache (KVQCache) as bf16 [B, T, H_kv, D]: the T newest tokens of each
+    sequence (token i at position cache_seqlens[b] - T + i; 0 where that is below 0), or without cache_seqlens the
+    positions 0 .. T - 1 (T: the whole cache by default). Returns (k, v)."""
+    lib = load_library()
+    ptrs, B, Hkv, Tk, bits, group, dev = _check_kvq(cache)
+    _require_cuda("k_codes", cache[0])
+    T = Tk if T is None else int(T)
+    if T < 1 or (cache_seqlens is None and T > Tk):
+        raise ValueError(f"T must be >= 1, and at most the cache's {Tk} positions without cache_seqlens")
+    if cache_seqlens is not None:
+        _check_seqlens(cache_seqlens, B, dev)
+    shape = (B, T, Hkv, 128)
+    # outputs made here belong to the stream that fills them
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+        _check_qkv("k", k, shape, dev)
+        _check_qkv("v", v, shape, dev)
+        st = lib.attn_kvq_read(*ptrs, None if cache_seqlens is None else cache_seqlens.data_ptr(), k.data_ptr(),
+                               v.data_ptr(), B, T, Hkv, Tk, 128, bits, group, _stream_handle(stream, dev))
+    _check("attn_kvq_read", st)
+    return k, v
+
+
+def attn_decode_kvq(q: torch.Tensor, cache, cache_seqlens: torch.Tensor, scale: Optional[float] = None,
+                    o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                    window: Optional[int] = None):
+    """attn_decode over a quantised cache (KVQCache): attention of Tq new queries q, bf16 [B, Tq, H, D], to the keys
+    and values the codes stand for. cache_seqlens, grouped heads and window as for attn_decode. Returns
+    (o [B, Tq, H, D], lse [B, H, Tq])."""
+    lib = load_library()
+    _require_cuda("q", q)
+    _check_qkv("q", q)
+    ptrs, B, Hkv, Tk, bits, group, dev = _check_kvq(cache)
+    Bq, Tq, H, D = q.shape
+    if q.device != dev:
+        raise ValueError(f"q is on {q.device}; every tensor of one call must be on {dev}")
+    if Bq != B:
+        raise ValueError(f"q has shape {tuple(q.shape)}; expected [{B}, Tq, H, {D}]")
+    _check_seqlens(cache_seqlens, B, dev)
+    scale = default_scale(D) if scale is None else float(scale)
+    win = _window_arg(window)
+    # outputs and workspace made here belong to the stream that uses them
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        o = torch.empty_like(q) if o is None else o
+        _check_qkv("o", o, q.shape, dev)
+        if lse is None:
+            lse = torch.empty((B, H, Tq), dtype=torch.float32, device=dev)
+        _check_f32("lse", lse, (B, H, Tq), dev)
+        if workspace is None:
+            workspace = torch.empty(max(int(lib.attn_decode_kvq_workspace_bytes(B, H, Hkv, Tq, Tk, D)), 16),
+                                    dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {dev}, like every tensor of one call")
+        st = lib.attn_decode_kvq(q.data_ptr(), *ptrs, cache_seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, H, Hkv, Tq,
+                                 Tk, D, bits, group, scale, win, _stream_handle(stream, dev))
+    _check("attn_decode_kvq", st)
+    return o, lse
+
+
 ROPE_PAIRINGS = {"interleaved": 0, "half": 1}
 
 
@@ -464,6 +611,7 @@ def causal_attention(q, k, v, scale: Optional[float] = None, window: Optional[in
 
 
 __all__ = ["attn_fwd", "attn_bwd", "attn_decode", "attn_bwd_workspace_bytes", "causal_attention", "CausalAttentionFunction",
+           "KVQCache", "kvq_cache", "kvq_write", "kvq_read", "attn_decode_kvq",
            "qk_norm_rope", "qk_norm_rope_bwd", "QKNormRopeFunction", "qk_norm_rope_attention",
            "get_device_error", "clear_device_error", "set_wait_limit_ns", "selftest_wait_timeout", "AttnError",
            "load_library", "LIB_PATH", "SIGNATURES"]

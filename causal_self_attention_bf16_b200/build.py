@@ -18,8 +18,9 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libattn.so")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libattn_debug.so")
-SOURCES = ["attn_api.cu", "attn_rope.cu"]
-DEPENDS = ["attn_api.cu", "attn_rope.cu", "attn_fwd.cuh", "attn_bwd.cuh", "attn_decode.cuh", "attn_common.cuh", "attn_errors.h", "sm100.cuh"]
+SOURCES = ["attn_api.cu", "attn_rope.cu", "attn_kvq.cu"]
+DEPENDS = SOURCES + ["attn_fwd.cuh", "attn_bwd.cuh", "attn_decode.cuh", "attn_kvq_decode.cuh", "attn_common.cuh",
+                     "attn_errors.h", "sm100.cuh"]
 
 
 def nvcc_path() -> str:

@@ -425,7 +425,10 @@ attn_status attn_get_device_error(uint32_t* word) {
   uint32_t rope_word = 0;
   e = static_cast<cudaError_t>(attn::rope_error_word(&rope_word));
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol(g_rope_error)");
-  *word |= rope_word;
+  uint32_t kvq_word = 0;
+  e = static_cast<cudaError_t>(attn::kvq_error_word(&kvq_word));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol(g_kvq_error)");
+  *word |= rope_word | kvq_word;
   if (*word & sm100::DEV_ERR_TIMEOUT) return ATTN_ERR_TIMEOUT;
   return *word ? ATTN_ERR_BOUNDS : ATTN_OK;
 }
@@ -436,6 +439,8 @@ attn_status attn_clear_device_error(void) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyToSymbol(g_device_error)");
   e = static_cast<cudaError_t>(attn::rope_error_clear());
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyToSymbol(g_rope_error)");
+  e = static_cast<cudaError_t>(attn::kvq_error_clear());
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyToSymbol(g_kvq_error)");
   e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
   return ATTN_OK;

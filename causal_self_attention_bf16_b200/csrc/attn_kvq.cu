@@ -1,0 +1,387 @@
+// The quantised key/value cache: new rows written as 4- or 8-bit codes (attn_kvq_write), rows read back as bf16
+// (attn_kvq_read), and cached decode over it (attn_decode_kvq, attn_kvq_decode.cuh). The format is in
+// include/attn.h: per group of `group` dims of a head vector, codes n, a bf16 scale s and a bf16 zero z stand for
+// n * s + z, with
+//   z = min(x),   s = fp32 quotient (max(x) - z) / (2^bits - 1), rounded up to bf16,   n = rint((x - z) / s).
+// The minimum of bf16 numbers is one of them, so z is exact; s is rounded up so that no code needs clamping below
+// its value (|n s + z - x| <= s / 2). Every step is one correctly rounded fp32 operation, so the codes are defined
+// bit for bit. A group that holds a NaN or an infinity, or whose max - min overflows fp32, gets s = z = NaN.
+//
+// Write and read are HBM-bound copies with a few operations per value. A thread owns 8 of a row's 128 dims, of the
+// key and the value row alike: 16 threads cover a row, so a half-warp reads (writes) 256 contiguous bytes of bf16
+// and writes (reads) 64 or 128 contiguous bytes of codes.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+#include <type_traits>
+
+#include "attn.h"
+#include "attn_errors.h"
+#include "attn_kvq_decode.cuh"
+
+using attn::g_kvq_error;
+
+namespace {
+
+using attn::g_cuda_error;
+
+constexpr int kCopyThreads = 256;
+constexpr int kChunks = 16;  // threads per row, 8 dims each
+enum : uint32_t {
+  kSiteKvqNew = 0xa0, kSiteKvqCodes = 0xa1, kSiteKvqParams = 0xa2, kSiteKvqOut = 0xa3
+};
+
+struct CopyParams {
+  const __nv_bfloat16* x[2];  // write: new key and value rows [B, T, H_kv, 128]
+  __nv_bfloat16* y[2];        // read: key and value rows [B, T, H_kv, 128]
+  uint8_t* codes[2];          // [B, H_kv, Tk, 128 * bits / 8]
+  uint32_t* params[2];        // [B, H_kv, Tk, 128 / group] words: s in the low half, z in the high half
+  const int* seqlens;         // [B]; read: null for rows from position 0 on
+  int B, T, Hkv, Tk;
+};
+
+// Row r of [B, T, H_kv] (token i of sequence b, head h): its cache row, or -1 where the token has no position.
+__device__ __forceinline__ long long cache_row(const CopyParams& p, int r) {
+  const int h = r % p.Hkv, bi = r / p.Hkv, b = bi / p.T, i = bi % p.T;
+  int pos = i;
+  if (p.seqlens) pos += min(max(p.seqlens[b], 0), p.Tk) - p.T;
+  return pos < 0 ? -1 : (static_cast<long long>(b) * p.Hkv + h) * p.Tk + pos;
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Quantise this thread's 8 dims, in a group that spans kGroup / 8 neighbouring threads. Returns the codes
+// (4 bits: word 0, nibble i = dim i; 8 bits: words 0 and 1, byte i = dim i) and the group's (s, z) word.
+template <int kBits, int kGroup>
+__device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t* sz) {
+  constexpr float kLevels = kBits == 4 ? 15.f : 255.f;
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  // min and max of bf16 pairs; a NaN anywhere in the group wins
+  __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(as_bf162(w[0]), as_bf162(w[1])),
+                                  __hmin2_nan(as_bf162(w[2]), as_bf162(w[3])));
+  __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(as_bf162(w[0]), as_bf162(w[1])),
+                                  __hmax2_nan(as_bf162(w[2]), as_bf162(w[3])));
+#pragma unroll
+  for (int m = 1; m < kGroup / 8; m <<= 1) {
+    mn = __hmin2_nan(mn, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mn), m)));
+    mx = __hmax2_nan(mx, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mx), m)));
+  }
+  const __nv_bfloat16 zb = __hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn));
+  const float z = __bfloat162float(zb);
+  const float span = __bfloat162float(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx))) - z;
+  if (!(span < INFINITY)) {  // a NaN or an infinity in the group, or a range past fp32: NaN throughout
+    *sz = 0x7fff7fffu;
+    return make_uint2(0u, 0u);
+  }
+  const uint32_t sbits = (__float_as_uint(__fdiv_rn(span, kLevels)) + 0xffffu) & 0xffff0000u;  // up to bf16
+  const float s = __uint_as_float(sbits);
+  *sz = (sbits >> 16) | (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
+  uint32_t n[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = (i & 1) ? hi_f32(w[i / 2]) : lo_f32(w[i / 2]);
+    const float q = sbits ? __fdiv_rn(x - z, s) : 0.f;
+    n[i] = static_cast<uint32_t>(fminf(rintf(q), kLevels));
+  }
+  uint2 c = make_uint2(0u, 0u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (kBits == 4) c.x |= n[i] << (4 * i);
+    else if (i < 4) c.x |= n[i] << (8 * i);
+    else c.y |= n[i] << (8 * (i - 4));
+  }
+  return c;
+}
+
+template <int kBits, int kGroup>
+__global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(const CopyParams p) {
+  constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
+  const int c = threadIdx.x % kChunks;
+  const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
+  const unsigned long long n_new = static_cast<unsigned long long>(rows) * 128;
+  const unsigned long long n_cache = static_cast<unsigned long long>(p.B) * p.Hkv * p.Tk;
+  (void)n_new, (void)n_cache;
+  const long long r = static_cast<long long>(blockIdx.x) * (kCopyThreads / kChunks) + threadIdx.x / kChunks;
+  const long long row = r < rows ? cache_row(p, static_cast<int>(r)) : -1;  // every lane stays for the shuffles
+  uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    if (row >= 0 && ATTN_IN_RANGE(r * 128 + 8 * c, 8, n_new, kSiteKvqNew, &g_kvq_error))
+      raw[t] = *reinterpret_cast<const uint4*>(p.x[t] + r * 128 + 8 * c);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    uint32_t sz;
+    const uint2 codes = quantise8<kBits, kGroup>(raw[t], &sz);
+    if (row < 0) continue;
+    if (ATTN_IN_RANGE(row * kRowBytes + c * kBits, kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error)) {
+      uint8_t* to = p.codes[t] + row * kRowBytes + c * kBits;
+      if constexpr (kBits == 4) *reinterpret_cast<uint32_t*>(to) = codes.x;
+      else *reinterpret_cast<uint2*>(to) = codes;
+    }
+    if ((8 * c) % kGroup == 0 &&
+        ATTN_IN_RANGE(row * kGroups + 8 * c / kGroup, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error))
+      p.params[t][row * kGroups + 8 * c / kGroup] = sz;
+  }
+}
+
+template <int kBits, int kGroup>
+__global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(const CopyParams p) {
+  constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
+  const int c = threadIdx.x % kChunks;
+  const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
+  const unsigned long long n_out = static_cast<unsigned long long>(rows) * 128;
+  const unsigned long long n_cache = static_cast<unsigned long long>(p.B) * p.Hkv * p.Tk;
+  (void)n_out, (void)n_cache;
+  const long long r = static_cast<long long>(blockIdx.x) * (kCopyThreads / kChunks) + threadIdx.x / kChunks;
+  if (r >= rows) return;
+  const long long row = cache_row(p, static_cast<int>(r));
+  uint2 codes[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+  uint32_t sz[2] = {0u, 0u};  // s = z = 0: rows without a position read as 0
+  if (row >= 0) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (ATTN_IN_RANGE(row * kRowBytes + c * kBits, kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error)) {
+        const uint8_t* from = p.codes[t] + row * kRowBytes + c * kBits;
+        if constexpr (kBits == 4) codes[t].x = *reinterpret_cast<const uint32_t*>(from);
+        else codes[t] = *reinterpret_cast<const uint2*>(from);
+      }
+      if (ATTN_IN_RANGE(row * kGroups + 8 * c / kGroup, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error))
+        sz[t] = p.params[t][row * kGroups + 8 * c / kGroup];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const float s = lo_f32(sz[t]), z = hi_f32(sz[t]);
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      uint32_t n0, n1;
+      if constexpr (kBits == 4) n0 = (codes[t].x >> (4 * i)) & 15u, n1 = (codes[t].x >> (4 * i + 4)) & 15u;
+      else {
+        const uint32_t w = i < 4 ? codes[t].x : codes[t].y;
+        n0 = (w >> (8 * (i % 4))) & 255u, n1 = (w >> (8 * (i % 4) + 8)) & 255u;
+      }
+      out[i / 2] = as_u32(__floats2bfloat162_rn(fmaf(static_cast<float>(n0), s, z), fmaf(static_cast<float>(n1), s, z)));
+    }
+    if (ATTN_IN_RANGE(r * 128 + 8 * c, 8, n_out, kSiteKvqOut, &g_kvq_error))
+      *reinterpret_cast<uint4*>(p.y[t] + r * 128 + 8 * c) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------- host side
+
+attn_status cuda_fail(cudaError_t e, const char* what) {
+  std::snprintf(g_cuda_error, attn::kErrorTextBytes, "%s: %s", what, cudaGetErrorString(e));
+  return ATTN_ERR_CUDA;
+}
+
+struct Range {
+  uintptr_t lo, hi;
+};
+Range span(const void* p, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, a + bytes};
+}
+bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// No output may overlap an input or another output.
+template <int kIns, int kOuts>
+bool any_overlap(const Range (&ins)[kIns], const Range (&outs)[kOuts]) {
+  for (int i = 0; i < kOuts; ++i) {
+    for (int j = 0; j < kIns; ++j)
+      if (overlap(outs[i], ins[j])) return true;
+    for (int j = i + 1; j < kOuts; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+  }
+  return false;
+}
+
+attn_status check_format(int D, int bits, int group) {
+  if (D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (bits != 4 && bits != 8) return ATTN_ERR_UNSUPPORTED;
+  if (group != 32 && group != 64 && group != 128) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+attn_status check_copy(int B, int T, int H_kv, int Tk, int D, int bits, int group) {
+  if (B < 1 || T < 1 || H_kv < 1 || Tk < 1) return ATTN_ERR_INVALID_ARG;
+  const attn_status st = check_format(D, bits, group);
+  if (st != ATTN_OK) return st;
+  // rows and cache rows are counted in 31 and 40 bits; byte offsets in 64
+  if (static_cast<long long>(B) * T > 0x7fffffffLL / H_kv) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * H_kv > (1LL << 40) / Tk) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+size_t codes_bytes(int B, int H_kv, int Tk, int bits) { return static_cast<size_t>(B) * H_kv * Tk * 16 * bits; }
+size_t params_bytes(int B, int H_kv, int Tk, int group) { return static_cast<size_t>(B) * H_kv * Tk * (512 / group); }
+
+// Calls f with the format as compile-time constants.
+template <typename F>
+void with_format(int bits, int group, F&& f) {
+  using std::integral_constant;
+  auto by_group = [&](auto b) {
+    if (group == 32) f(b, integral_constant<int, 32>());
+    else if (group == 64) f(b, integral_constant<int, 64>());
+    else f(b, integral_constant<int, 128>());
+  };
+  if (bits == 4) by_group(integral_constant<int, 4>());
+  else by_group(integral_constant<int, 8>());
+}
+
+attn_status launch_copy(bool write, const CopyParams& p, int bits, int group, void* stream) {
+  const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
+  const unsigned grid = static_cast<unsigned>((rows + kCopyThreads / kChunks - 1) / (kCopyThreads / kChunks));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  with_format(bits, group, [&](auto b, auto g) {
+    if (write) kvq_write_kernel<b.value, g.value><<<grid, kCopyThreads, 0, s>>>(p);
+    else kvq_read_kernel<b.value, g.value><<<grid, kCopyThreads, 0, s>>>(p);
+  });
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, write ? "kvq_write_kernel launch" : "kvq_read_kernel launch");
+  return ATTN_OK;
+}
+
+attn_status check_decode(int B, int H, int Hkv, int Tq, int Tk, int D, int bits, int group, float scale) {
+  if (B < 1 || H < 1 || Tq < 1 || Tk < 1) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (Hkv < 1 || Hkv > H || H % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  const attn_status st = check_format(D, bits, group);
+  if (st != ATTN_OK) return st;
+  if ((H / Hkv) * static_cast<long long>(Tq) > attn::kKvqMaxRows) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * H * Tq > 0x7fffffffLL / 8) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hkv > (1LL << 40) / Tk) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_kvq_write(const void* k, const void* v, void* k_codes, void* k_params, void* v_codes,
+                           void* v_params, const int* cache_seqlens, int B, int T, int H_kv, int Tk, int D, int bits,
+                           int group, void* stream) {
+  if (!k || !v || !k_codes || !k_params || !v_codes || !v_params || !cache_seqlens) return ATTN_ERR_INVALID_ARG;
+  const attn_status st = check_copy(B, T, H_kv, Tk, D, bits, group);
+  if (st != ATTN_OK) return st;
+  for (const void* ptr : {k, v, static_cast<const void*>(k_codes), static_cast<const void*>(k_params),
+                          static_cast<const void*>(v_codes), static_cast<const void*>(v_params)})
+    if (!aligned(ptr, 16)) return ATTN_ERR_MISALIGNED;
+  if (!aligned(cache_seqlens, 4)) return ATTN_ERR_MISALIGNED;
+  const size_t xb = static_cast<size_t>(B) * T * H_kv * 256;
+  const size_t cb = codes_bytes(B, H_kv, Tk, bits), pb = params_bytes(B, H_kv, Tk, group);
+  const Range ins[3] = {span(k, xb), span(v, xb), span(cache_seqlens, static_cast<size_t>(B) * 4)};
+  const Range outs[4] = {span(k_codes, cb), span(k_params, pb), span(v_codes, cb), span(v_params, pb)};
+  if (any_overlap(ins, outs)) return ATTN_ERR_INVALID_ARG;
+  CopyParams p{};
+  p.x[0] = static_cast<const __nv_bfloat16*>(k);
+  p.x[1] = static_cast<const __nv_bfloat16*>(v);
+  p.codes[0] = static_cast<uint8_t*>(k_codes);
+  p.codes[1] = static_cast<uint8_t*>(v_codes);
+  p.params[0] = static_cast<uint32_t*>(k_params);
+  p.params[1] = static_cast<uint32_t*>(v_params);
+  p.seqlens = cache_seqlens;
+  p.B = B, p.T = T, p.Hkv = H_kv, p.Tk = Tk;
+  return launch_copy(true, p, bits, group, stream);
+}
+
+attn_status attn_kvq_read(const void* k_codes, const void* k_params, const void* v_codes, const void* v_params,
+                          const int* cache_seqlens, void* k, void* v, int B, int T, int H_kv, int Tk, int D,
+                          int bits, int group, void* stream) {
+  if (!k || !v || !k_codes || !k_params || !v_codes || !v_params) return ATTN_ERR_INVALID_ARG;
+  const attn_status st = check_copy(B, T, H_kv, Tk, D, bits, group);
+  if (st != ATTN_OK) return st;
+  if (!cache_seqlens && T > Tk) return ATTN_ERR_INVALID_ARG;
+  for (const void* ptr : {k_codes, k_params, v_codes, v_params, static_cast<const void*>(k),
+                          static_cast<const void*>(v)})
+    if (!aligned(ptr, 16)) return ATTN_ERR_MISALIGNED;
+  if (!aligned(cache_seqlens, 4)) return ATTN_ERR_MISALIGNED;
+  const size_t xb = static_cast<size_t>(B) * T * H_kv * 256;
+  const size_t cb = codes_bytes(B, H_kv, Tk, bits), pb = params_bytes(B, H_kv, Tk, group);
+  const Range ins[5] = {span(k_codes, cb), span(k_params, pb), span(v_codes, cb), span(v_params, pb),
+                        span(cache_seqlens, cache_seqlens ? static_cast<size_t>(B) * 4 : 0)};
+  const Range outs[2] = {span(k, xb), span(v, xb)};
+  if (any_overlap(ins, outs)) return ATTN_ERR_INVALID_ARG;
+  CopyParams p{};
+  p.y[0] = static_cast<__nv_bfloat16*>(k);
+  p.y[1] = static_cast<__nv_bfloat16*>(v);
+  p.codes[0] = const_cast<uint8_t*>(static_cast<const uint8_t*>(k_codes));
+  p.codes[1] = const_cast<uint8_t*>(static_cast<const uint8_t*>(v_codes));
+  p.params[0] = const_cast<uint32_t*>(static_cast<const uint32_t*>(k_params));
+  p.params[1] = const_cast<uint32_t*>(static_cast<const uint32_t*>(v_params));
+  p.seqlens = cache_seqlens;
+  p.B = B, p.T = T, p.Hkv = H_kv, p.Tk = Tk;
+  return launch_copy(false, p, bits, group, stream);
+}
+
+size_t attn_decode_kvq_workspace_bytes(int B, int H, int H_kv, int Tq, int Tk, int D) {
+  if (check_decode(B, H, H_kv, Tq, Tk, D, 4, 128, 1.0f) != ATTN_OK) return 0;
+  return 16;
+}
+
+int attn_decode_kvq_kernels(int B, int H, int H_kv, int Tq, int Tk, int D, int window) {
+  if (check_decode(B, H, H_kv, Tq, Tk, D, 4, 128, 1.0f) != ATTN_OK || window < -1) return 0;
+  return 1;
+}
+
+attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
+                            const void* v_params, const int* cache_seqlens, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, int B, int H, int H_kv, int Tq, int Tk, int D, int bits,
+                            int group, float scale, int window, void* stream) {
+  if (!q || !k_codes || !k_params || !v_codes || !v_params || !cache_seqlens || !o || !lse)
+    return ATTN_ERR_INVALID_ARG;
+  const attn_status st = check_decode(B, H, H_kv, Tq, Tk, D, bits, group, scale);
+  if (st != ATTN_OK) return st;
+  if (window < -1) return ATTN_ERR_INVALID_ARG;
+  const size_t need = attn_decode_kvq_workspace_bytes(B, H, H_kv, Tq, Tk, D);
+  if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+  for (const void* ptr : {q, k_codes, k_params, v_codes, v_params, static_cast<const void*>(o),
+                          static_cast<const void*>(workspace)})
+    if (!aligned(ptr, 16)) return ATTN_ERR_MISALIGNED;
+  if (!aligned(lse, 4) || !aligned(cache_seqlens, 4)) return ATTN_ERR_MISALIGNED;
+  const size_t qb = static_cast<size_t>(B) * Tq * H * 256;
+  const size_t cb = codes_bytes(B, H_kv, Tk, bits), pb = params_bytes(B, H_kv, Tk, group);
+  const Range ins[6] = {span(q, qb), span(k_codes, cb), span(k_params, pb), span(v_codes, cb), span(v_params, pb),
+                        span(cache_seqlens, static_cast<size_t>(B) * 4)};
+  const Range outs[3] = {span(o, qb), span(lse, static_cast<size_t>(B) * H * Tq * 4), span(workspace, need)};
+  if (any_overlap(ins, outs)) return ATTN_ERR_INVALID_ARG;
+  attn::KvqDecodeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_codes = static_cast<const uint8_t*>(k_codes);
+  p.v_codes = static_cast<const uint8_t*>(v_codes);
+  p.k_params = static_cast<const uint32_t*>(k_params);
+  p.v_params = static_cast<const uint32_t*>(v_params);
+  p.seqlens = cache_seqlens;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.B = B, p.H = H, p.Hkv = H_kv, p.Tq = Tq, p.Tk = Tk;
+  p.window = window;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  with_format(bits, group, [&](auto b, auto g) {
+    attn::kvq_decode_rows_kernel<b.value, g.value><<<static_cast<unsigned>(B * H * Tq), 128, 0, s>>>(p);
+  });
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_decode_rows_kernel launch");
+  return ATTN_OK;
+}
+
+}  // extern "C"
+
+namespace attn {
+// Read and clear this unit's device error word (synchronous; the caller has synchronised the device).
+int kvq_error_word(uint32_t* word) {
+  return static_cast<int>(cudaMemcpyFromSymbol(word, g_kvq_error, sizeof(uint32_t)));
+}
+int kvq_error_clear() {
+  const uint32_t zero = 0;
+  return static_cast<int>(cudaMemcpyToSymbol(g_kvq_error, &zero, sizeof(uint32_t)));
+}
+}  // namespace attn

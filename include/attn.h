@@ -17,8 +17,8 @@
  * Conventions for every entry point
  *   - Tensors are device pointers. q, k, v, o, dO, dq, dk, dv: bf16, [B, T, H, D] contiguous (D fastest).
  *     lse: fp32 [B, H, T] contiguous. Every pointer must be 16-byte aligned (TMA requirement), except the
- *     int32 / fp32 vectors of attn_decode (lse, cache_seqlens) and attn_qk_norm_rope[_bwd] (pos_offsets),
- *     which need 4 bytes.
+ *     int32 / fp32 vectors of attn_decode and the attn_kvq calls (lse, cache_seqlens) and of
+ *     attn_qk_norm_rope[_bwd] (pos_offsets), which need 4 bytes.
  *   - The caller owns and allocates every buffer, including the backward workspace. The library never
  *     allocates, frees or synchronises; all work is enqueued asynchronously on `stream` (a cudaStream_t;
  *     NULL = legacy default stream) on the current CUDA device.
@@ -40,7 +40,7 @@ extern "C" {
 typedef enum {
   ATTN_OK = 0,
   ATTN_ERR_INVALID_ARG = 1,  /* null pointer, non-positive size, non-finite or non-positive scale, overlap */
-  ATTN_ERR_UNSUPPORTED = 2,  /* D != 128, or sizes beyond the kernels' index range */
+  ATTN_ERR_UNSUPPORTED = 2,  /* D != 128, sizes beyond the kernels' index range, or a cache format that is not held */
   ATTN_ERR_MISALIGNED = 3,   /* a pointer is not 16-byte aligned */
   ATTN_ERR_CUDA = 4,         /* a CUDA runtime/driver call or a launch failed; see attn_last_cuda_error() */
   ATTN_ERR_TIMEOUT = 5,      /* a kernel gave up on a bounded wait (reported by attn_get_device_error) */
@@ -233,6 +233,65 @@ attn_status attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_o
                                   float rope_base, float eps, int pairing, void* stream);
 
 /*
+ * Quantised key/value cache. The inference engine's decode reads the whole cache once per token and is bound by
+ * its bytes (apidog "Train your own ChatGPT", section 6 "Inference engine"); here the cache is held in 4 or 8 bits.
+ * The pages have no counterpart: this is an addition of this library.
+ *
+ * Format. A row is one key or value head vector x of 128 bf16 dims, held in groups of `group` (32, 64 or 128) dims.
+ * A group holds unsigned codes n of `bits` (4 or 8) bits, a bf16 scale s and a bf16 zero z, and stands for n * s + z:
+ *   z = min(x)                                            (one of the group's numbers, so exact)
+ *   s = (max(x) - z) / (2^bits - 1), one fp32 quotient, rounded up to bf16
+ *   n = (x - z) / s in fp32, rounded to the nearest integer, ties to even     (0 when s = 0)
+ * so |n s + z - x| <= s / 2 up to fp32 rounding. A group with a NaN or an infinity, or whose max - min overflows
+ * fp32, has s = z = NaN and reads as NaN throughout. Subnormal numbers are kept.
+ * Buffers, for B sequences, H_kv heads and room for Tk positions (head-major, so that one head's keys are one
+ * stream of memory); each 16-byte aligned:
+ *   codes  : uint8 [B, H_kv, Tk, 128 * bits / 8], in dim order; with 4 bits the even dim is the low half of its byte
+ *   params : bf16  [B, H_kv, Tk, 128 / group, 2], (s, z)
+ * Rows that were never written may hold anything.
+ *
+ * cache_seqlens: device int32 [B], the valid keys of each sequence, the new tokens included, as for attn_decode
+ * (values outside [0, Tk] are clamped). The i-th of a call's T newest tokens of sequence b has position
+ * L_b - T + i; tokens whose position is below 0 (left padding) are not there.
+ *
+ * attn_kvq_write: quantise the new tokens' keys and values into the cache.
+ *   k, v in : bf16 [B, T, H_kv, D];  k_codes, k_params, v_codes, v_params : the cache
+ * Every row outside the written positions is left as it is. One kernel launch.
+ *
+ * attn_kvq_read: the T newest tokens' keys and values read back, bf16(n * s + z); rows of tokens that are not there
+ * are 0. cache_seqlens = NULL: positions 0 .. T - 1 of every sequence instead (T <= Tk, else ATTN_ERR_INVALID_ARG).
+ *   k, v out : bf16 [B, T, H_kv, D].  One kernel launch.
+ *
+ * T >= 1; bits, group and D as above, else ATTN_ERR_UNSUPPORTED. Calls on one cache must be ordered by stream
+ * or event, like any write and read of one buffer.
+ */
+attn_status attn_kvq_write(const void* k, const void* v, void* k_codes, void* k_params, void* v_codes,
+                           void* v_params, const int* cache_seqlens, int B, int T, int H_kv, int Tk, int D, int bits,
+                           int group, void* stream);
+attn_status attn_kvq_read(const void* k_codes, const void* k_params, const void* v_codes, const void* v_params,
+                          const int* cache_seqlens, void* k, void* v, int B, int T, int H_kv, int Tk, int D,
+                          int bits, int group, void* stream);
+
+/*
+ * attn_decode_ex over the quantised cache: attention of Tq new queries to the keys and values n * s + z that the
+ * codes stand for (not rounded to bf16 in between). Forward only.
+ *   q in : bf16 [B, Tq, H, D];  o out : bf16 [B, Tq, H, D];  lse out : fp32 [B, H, Tq]
+ *   window, scale, cache_seqlens, grouped heads, the row limit (H / H_kv) * Tq <= 32 and queries that see no key
+ *   (o = 0, lse = -inf): as for attn_decode_ex. Rows of the cache that no query sees are never used, whatever they
+ *   hold. A NaN in a key that a query sees makes that query's o and lse NaN, one in a value its o, in the group's dims.
+ *   workspace scratch : attn_decode_kvq_workspace_bytes(B, H, H_kv, Tq, Tk, D) bytes, 16-byte aligned, for any
+ *   window, bits and group; its contents on entry do not matter. Calls sharing a workspace must not overlap in time
+ *   on the GPU.
+ * attn_decode_kvq_kernels: the kernels one call launches (0 for arguments the call rejects). Host-only.
+ */
+size_t attn_decode_kvq_workspace_bytes(int B, int H, int H_kv, int Tq, int Tk, int D);
+int attn_decode_kvq_kernels(int B, int H, int H_kv, int Tq, int Tk, int D, int window);
+attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
+                            const void* v_params, const int* cache_seqlens, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, int B, int H, int H_kv, int Tq, int Tk, int D, int bits,
+                            int group, float scale, int window, void* stream);
+
+/*
  * Device-side error word of the kernels of this library on the current device since the last clear: 0, or the
  * OR of (site << 8) | kind over what went wrong, kind 1 = a kernel gave up on a bounded wait, kind 2 = (debug
  * build only) a kernel's address check failed and the access was skipped; the site bits name the wait or the
@@ -261,7 +320,8 @@ attn_status attn_selftest_wait_timeout(uint64_t limit_ns, void* stream);
 /*
  * Debug build. libattn_debug.so is this library compiled with -DATTN_DEBUG: every kernel access through a plain
  * address (the ones no TMA tensor map bounds: LSE/Delta rows, dQ accumulator reductions and conversion, the
- * forward's LSE, the decode kernels' cache, partial and output rows, the prologue's rows) is first checked
+ * forward's LSE, the decode kernels' cache, partial and output rows, the prologue's rows, the quantised cache's rows)
+ * is first checked
  * against the extent of its array; a failed check sets kind 2 in the device error word and skips the access.
  * Same symbols, same results, slower. attn_is_debug_build() returns 1 in it, 0 in libattn.so.
  * attn_selftest_bounds_check() launches one checked store past its array's declared extent (debug build: the

@@ -167,3 +167,41 @@ def test_debug_build_matches_release_on_the_prologue(libs, pairing):
     assert _error_word(debug) == (0, 0), "an address check fired on valid inputs"
     for name, a, b in zip(("q_out", "k_out", "dq", "dk"), ref, got):
         assert torch.equal(a, b), f"prologue {name} differs between the builds"
+
+
+def _kvq(lib, q, k, v, cache, lens, bits, group, window):
+    """Write, read back and decode through one build; returns the cache's buffers and every output."""
+    s = torch.cuda.current_stream().cuda_stream
+    B, T, Hkv, Tk = k.shape[0], k.shape[1], k.shape[2], cache[0].shape[2]
+    Tq, H = q.shape[1], q.shape[2]
+    cache = [t.clone() for t in cache]
+    ptrs = [t.data_ptr() for t in cache]
+    assert lib.attn_kvq_write(k.data_ptr(), v.data_ptr(), *ptrs, lens.data_ptr(), B, T, Hkv, Tk, 128, bits, group, s) == 0
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    assert lib.attn_kvq_read(*ptrs, lens.data_ptr(), ko.data_ptr(), vo.data_ptr(), B, T, Hkv, Tk, 128, bits, group, s) == 0
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
+    wsb = lib.attn_decode_kvq_workspace_bytes(B, H, Hkv, Tq, Tk, 128)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=q.device)
+    assert lib.attn_decode_kvq(q.data_ptr(), *ptrs, lens.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), wsb, B,
+                               H, Hkv, Tq, Tk, 128, bits, group, 128 ** -0.5, window, s) == 0
+    torch.cuda.synchronize()
+    return [*cache, ko, vo, o, lse]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits,group,H,Tq,window", [(4, 32, 4, 2, -1), (8, 128, 16, 2, -1), (4, 64, 10, 1, 100)])
+def test_debug_build_matches_release_on_the_quantised_cache(libs, bits, group, H, Tq, window):
+    release, debug = libs
+    dev = torch.device("cuda:0")
+    g = torch.Generator().manual_seed(9 + bits)
+    B, Hkv, T, Tk = 3, 2, 700, 901
+    q, k, v = (_randn((B, n, h, 128), g, dev) for n, h in ((Tq, H), (T, Hkv), (T, Hkv)))
+    cache = attn.kvq_cache(B, Hkv, Tk, bits, group, dev)
+    lens = torch.tensor([Tk, 1, 333], dtype=torch.int32, device=dev)
+    assert debug.attn_clear_device_error() == 0
+    ref = _kvq(release, q, k, v, cache, lens, bits, group, window)
+    got = _kvq(debug, q, k, v, cache, lens, bits, group, window)
+    assert _error_word(debug) == (0, 0), "an address check fired on valid inputs"
+    for i, (a, b) in enumerate(zip(ref, got)):
+        assert torch.equal(a, b), f"output {i} differs between the builds"

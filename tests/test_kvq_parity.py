@@ -1,0 +1,454 @@
+"""The quantised key/value cache on the GPU, through the binding and the C ABI, against the float64 oracle.
+
+Tolerances, derived from the arithmetic:
+  codes, params : the device rounds max - z, x - z and both quotients to fp32. Params are equal to the oracle's. A
+            quotient below 256 is off by at most 256 * 3 * 2^-24 < 2^-14 (three roundings), so codes are equal
+            wherever the oracle's quotient is further than 2^-14 from a tie, and off by one at most elsewhere.
+  read    : bf16(fp32(n s + z)): n s is exact in fp32, one fp32 rounding (2^-24 of |n s| + |z|), one bf16 (2^-8 of the
+            value).
+  lse     : scores are fp32 sums of under 160 products (128 dims, the groups' terms), in any order and with each
+            partial sum rounded or truncated at 2^-23: off by at most dS = 160 * 2^-23 * A with A the sum of the
+            terms' sizes, scale * sum_d |q_d| (|z| + c s), where c = 2 * 2^bits covers codes that are carried with
+            an offset of up to 2^bits + 16. lse is off by the largest dS of its keys, plus the fp32 rounding of
+            the running max and sum (2^-20, and 2^-22 of its value).
+  o       : one bf16 rounding, 2^-8 |o|; each weight is off by 2 dS + 2^-14 of itself (exp2 and the running sums
+            in fp32, a weight carried to 16 bits), each counted against sum_j p_j (|z| + c s).
+"""
+import numpy as np
+import pytest
+import torch
+
+import causal_self_attention_bf16_b200 as attn
+from oracle import decode_forward_kvq, dequantize, quantize, unpack_codes
+
+pytestmark = pytest.mark.gpu
+
+BITS_GROUPS = [(b, g) for b in (4, 8) for g in (32, 64, 128)]
+
+
+def cpu(t):
+    return t.detach().to("cpu", torch.float64).numpy()
+
+
+def randn(shape, seed, rows=0.5):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g)
+    return (x * torch.exp(rows * torch.randn((*shape[:-1], 1), generator=g))).to(torch.bfloat16)
+
+
+def ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def clean():
+    torch.cuda.synchronize()
+    assert attn.get_device_error() == 0
+
+
+def poisoned(B, Hkv, Tk, bits, group, seed=0):
+    """A cache whose rows hold arbitrary codes and NaN params, as memory that was never written may."""
+    c = attn.kvq_cache(B, Hkv, Tk, bits, group)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for t in (c.k_codes, c.v_codes):
+        t.copy_(torch.randint(0, 256, t.shape, generator=g, device="cuda", dtype=torch.uint8))
+    c.k_params.fill_(float("nan"))
+    c.v_params.fill_(float("nan"))
+    return c
+
+
+def check_row(x, codes, params, bits, group, what):
+    """Rows x [..., 128] against their codes and params."""
+    n, s, z, tie = quantize(x, bits, group)
+    got = unpack_codes(codes.cpu().numpy(), bits)
+    p = cpu(params)
+    assert np.array_equal(p[..., 0], s, equal_nan=True) and np.array_equal(p[..., 1], z, equal_nan=True), what
+    off = np.abs(got - n)
+    assert (off <= 1).all() and (off[tie > 2.0 ** -14] == 0).all(), f"{what}: codes off by {off.max()}"
+
+
+# ---------------------------------------------------------------------------------------------- write
+
+@pytest.mark.parametrize("bits,group", BITS_GROUPS)
+@pytest.mark.parametrize("B,T,Hkv,Tk,lens", [
+    (1, 1, 1, 1, [1]),                       # the smallest call
+    (3, 1, 2, 40, [1, 17, 40]),              # one new token each
+    (2, 37, 3, 100, [37, 99]),               # a prompt, and tokens after others
+    (4, 9, 5, 9, [9, 4, 0, 1]),              # left padding, an empty sequence
+    (3, 20, 1, 12, [12, 40, -3]),            # more tokens than positions, lengths outside [0, Tk]
+])
+def test_write_matches_the_format(bits, group, B, T, Hkv, Tk, lens):
+    k, v = randn((B, T, Hkv, 128), 1).cuda(), randn((B, T, Hkv, 128), 2).cuda()
+    cache = poisoned(B, Hkv, Tk, bits, group)
+    before = [t.clone() for t in cache]
+    attn.kvq_write(cache, k, v, ints(lens))
+    clean()
+    written = torch.zeros((B, Hkv, Tk), dtype=torch.bool)
+    for b, L in enumerate(min(max(L, 0), Tk) for L in lens):
+        i0 = max(0, T - L)
+        written[b, :, L - T + i0:L] = True
+        for x, codes, params, name in ((k, *cache[:2], "k"), (v, *cache[2:], "v")):
+            check_row(x[b, i0:].cpu(), codes[b, :, L - T + i0:L].transpose(0, 1),
+                      params[b, :, L - T + i0:L].transpose(0, 1), bits, group, f"{name} b={b}")
+    for t, old in zip(cache, before):        # every other row is left as it was (bit for bit: NaN params too)
+        flat = lambda x: x.view(torch.uint8).cpu().reshape(B, Hkv, Tk, -1)[~written]  # noqa: E731
+        assert torch.equal(flat(t), flat(old))
+
+
+@pytest.mark.parametrize("bits,group", [(4, 32), (8, 128)])
+def test_write_unusual_rows(bits, group):
+    """Constant rows, grids that come back exactly, ties, NaN and infinities, overflowing and subnormal ranges."""
+    x = torch.zeros(12, 128)
+    x[1] = 3.5
+    x[2] = torch.arange(128).remainder(16) * 0.25 - 2
+    x[3] = torch.arange(128).remainder(31) * 0.5            # halves of the 4-bit step: ties
+    x[4, 7], x[5, 7], x[6, 7] = float("nan"), float("inf"), -float("inf")
+    x[7, 3], x[7, 4] = 3e38, -3e38
+    x[8, 0] = 1e-40
+    x[9] = torch.linspace(-1, 1, 128) * 1e-38
+    x[10] = torch.linspace(1, 2, 128) * 1e38
+    x[11, 64] = -1e-3
+    x = x.to(torch.bfloat16).reshape(1, 12, 1, 128).cuda()
+    cache = attn.kvq_cache(1, 1, 12, bits, group)
+    attn.kvq_write(cache, x, -x, ints([12]))
+    clean()
+    check_row(x[0, :, 0].cpu(), cache.k_codes[0, 0], cache.k_params[0, 0], bits, group, "k")
+    check_row(-x[0, :, 0].cpu(), cache.v_codes[0, 0], cache.v_params[0, 0], bits, group, "v")
+
+
+def test_write_many_rows():
+    """Enough rows for many blocks, checked against the oracle on a sample and for every row's error bound."""
+    B, T, Hkv, bits, group = 3, 701, 10, 4, 64
+    k, v = randn((B, T, Hkv, 128), 5).cuda(), randn((B, T, Hkv, 128), 6).cuda()
+    cache = attn.kvq_cache(B, Hkv, 900, bits, group)
+    attn.kvq_write(cache, k, v, ints([701, 800, 900]))
+    rk, rv = attn.kvq_read(cache, T, ints([701, 800, 900]))
+    clean()
+    for b, L in enumerate((701, 800, 900)):
+        for h in (0, 7):
+            check_row(k[b, :, h].cpu(), cache.k_codes[b, h, L - T:L], cache.k_params[b, h, L - T:L], bits, group, "k")
+    for x, y, p in ((k, rk, cache.k_params), (v, rv, cache.v_params)):
+        step = torch.stack([p[b, :, L - T:L, :, 0] for b, L in enumerate((701, 800, 900))]).transpose(1, 2).float()
+        bound = step.repeat_interleave(group, -1) / 2 + 2.0 ** -7 * x.float().abs() + 2.0 ** -8 * step.amax(-1, True)
+        assert ((x.float() - y.float()).abs() <= bound).all()
+
+
+# ---------------------------------------------------------------------------------------------- read
+
+@pytest.mark.parametrize("bits,group", BITS_GROUPS)
+@pytest.mark.parametrize("B,T,Hkv,Tk,lens", [
+    (1, 1, 1, 1, [1]), (1, 1, 1, 1, None), (3, 5, 2, 40, [5, 2, 40]), (2, 33, 3, 33, None), (2, 7, 5, 33, None),
+    (4, 50, 3, 20, [20, 0, -1, 99])])
+def test_read_matches_the_values(bits, group, B, T, Hkv, Tk, lens):
+    cache = poisoned(B, Hkv, Tk, bits, group, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for t in (cache.k_params, cache.v_params):
+        t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        t[..., 0].abs_()
+    out = [torch.full((B, T, Hkv, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    attn.kvq_read(cache, T, None if lens is None else ints(lens), *out)
+    clean()
+    for y, codes, params in ((out[0], *cache[:2]), (out[1], *cache[2:])):
+        ref = dequantize(codes.cpu().numpy(), params.cpu(), bits).transpose(0, 2, 1, 3)
+        size = (dequantize(codes.cpu().numpy(), params.cpu().abs(), bits)).transpose(0, 2, 1, 3)
+        for b in range(B):
+            L = T if lens is None else min(max(lens[b], 0), Tk)
+            i0 = max(0, T - L)
+            assert (cpu(y[b, :i0]) == 0).all()
+            r, z = ref[b, L - T + i0:L], size[b, L - T + i0:L]
+            assert (np.abs(cpu(y[b, i0:]) - r) <= 2.0 ** -8 * np.abs(r) + 2.0 ** -23 * z).all()
+
+
+def test_read_whole_cache_by_default():
+    cache = attn.kvq_cache(2, 3, 11, 8, 64)
+    k = randn((2, 11, 3, 128), 8).cuda()
+    attn.kvq_write(cache, k, k, ints([11, 11]))
+    a, b = attn.kvq_read(cache), attn.kvq_read(cache, 11, ints([11, 11]))
+    clean()
+    assert a[0].shape == (2, 11, 3, 128) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ---------------------------------------------------------------------------------------------- decode
+
+def filled(B, Hkv, Tk, bits, group, lens, seed, tail_nan=True):
+    """A cache holding random rows; past each sequence's length, rows of NaN params (never to be used)."""
+    cache = attn.kvq_cache(B, Hkv, Tk, bits, group)
+    attn.kvq_write(cache, randn((B, Tk, Hkv, 128), seed, 0.2).cuda(), randn((B, Tk, Hkv, 128), seed + 1).cuda(),
+                   ints([Tk] * B))
+    if tail_nan:
+        for b, L in enumerate(lens):
+            L = min(max(L, 0), Tk)
+            cache.k_params[b, :, L:] = float("nan")
+            cache.v_params[b, :, L:] = float("nan")
+            cache.k_codes[b, :, L:] = 255
+            cache.v_codes[b, :, L:] = 255
+    return cache
+
+
+def check_decode(q, cache, lens, scale, window, o, lse, what):
+    q64, (kc, kp, vc, vp) = cpu(q), [t.cpu() for t in cache]
+    B, Tq, H, D = q64.shape
+    Hkv, Tk, bits = kc.shape[1], kc.shape[2], kc.shape[3] * 8 // D
+    G = H // Hkv
+    o, lse = cpu(o), cpu(lse)
+    O, LSE = decode_forward_kvq(q64, (kc.numpy(), kp, vc.numpy(), vp), lens, scale, window)
+    c = 2.0 * 2 ** bits
+    for b, L in enumerate(min(max(L, 0), Tk) for L in lens):
+        for h in range(H):
+            k, v = (dequantize(t[b, h // G, :L].numpy(), p[b, h // G, :L], bits) for t, p in ((kc, kp), (vc, vp)))
+            ks, vs = (np.repeat(np.abs(cpu(p[b, h // G, :L, :, 1])) + c * cpu(p[b, h // G, :L, :, 0]), D // p.shape[3], -1)
+                      for p in (kp, vp))
+            for i in range(Tq):
+                last = L - Tq + i
+                w = f"{what} b={b} h={h} i={i}"
+                if last < 0:
+                    assert (o[b, i, h] == 0).all() and lse[b, h, i] == -np.inf, w
+                    continue
+                first = 0 if window is None else max(0, last - window)
+                dS = 160 * 2.0 ** -23 * scale * (ks[first:last + 1] @ np.abs(q64[b, i, h])).max()
+                assert abs(lse[b, h, i] - LSE[b, h, i]) <= dS + 2.0 ** -20 + 2.0 ** -22 * abs(LSE[b, h, i]), w
+                p = np.exp(scale * (k[first:last + 1] @ q64[b, i, h]) - LSE[b, h, i])
+                tol = 2.0 ** -8 * np.abs(O[b, i, h]) + (2 * dS + 2.0 ** -14) * (p @ vs[first:last + 1])
+                err = np.abs(o[b, i, h] - O[b, i, h])
+                assert (err <= tol).all(), f"{w}: {(err / tol).max():.2f} of the tolerance"
+
+
+def run_decode(B, H, Hkv, Tq, Tk, bits, group, lens, window=None, scale=128 ** -0.5, seed=10):
+    cache = filled(B, Hkv, Tk, bits, group, lens, seed)
+    q = randn((B, Tq, H, 128), seed + 2, 0.2).cuda()
+    o = torch.full_like(q, float("nan"))
+    lse = torch.full((B, H, Tq), float("nan"), device="cuda")
+    attn.attn_decode_kvq(q, cache, ints(lens), scale, o, lse, window=window)
+    clean()
+    check_decode(q, cache, lens, scale, window, o, lse, f"{B, H, Hkv, Tq, Tk, bits, group, lens, window}")
+    return q, cache, o, lse
+
+
+@pytest.mark.parametrize("bits,group", BITS_GROUPS)
+@pytest.mark.parametrize("B,H,Hkv,Tq,Tk,lens", [
+    (1, 1, 1, 1, 1, [1]),                                # one key
+    (3, 4, 2, 2, 300, [300, 1, 77]),                     # grouped heads, two tokens, one below position 0
+    (4, 3, 3, 1, 130, [0, 16, 17, 129]),                 # an empty sequence, lengths around a tile's ends
+    (2, 10, 2, 1, 999, [999, 640]),                      # five rows
+    (2, 8, 1, 4, 515, [515, 3]),                         # 32 rows
+    (1, 6, 2, 3, 64, [70]),                              # nine rows, a length past the capacity
+])
+def test_decode_matches_oracle(bits, group, B, H, Hkv, Tq, Tk, lens):
+    run_decode(B, H, Hkv, Tq, Tk, bits, group, lens)
+
+
+@pytest.mark.parametrize("R", [1, 2, 3, 4, 5, 7, 8, 9, 12, 15, 16, 17, 24, 25, 31, 32])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_decode_every_row_count(R, bits):
+    run_decode(2, R, 1, 1, 200, bits, 64, [200, 33], seed=R)
+
+
+@pytest.mark.parametrize("window", [0, 1, 15, 16, 100, 700, 5000])
+@pytest.mark.parametrize("bits,group", [(4, 64), (8, 32)])
+def test_decode_window(window, bits, group):
+    run_decode(3, 4, 2, 3, 700, bits, group, [700, 2, 333], window=window)
+
+
+@pytest.mark.parametrize("Tq", [2, 5, 16, 32])
+def test_decode_several_tokens(Tq):
+    run_decode(3, 2, 2, Tq, 100, 4, 32, [100, Tq, Tq // 2])
+
+
+@pytest.mark.parametrize("bits,group,Hkv,window", [(4, 32, 1, None), (8, 128, 2, None), (4, 64, 1, 3000)])
+def test_decode_long_cache(bits, group, Hkv, window):
+    """Few heads over a long cache: the work is split along it."""
+    run_decode(1, 2, Hkv, 1, 20011, bits, group, [19997], window=window)
+    run_decode(2, 2 * Hkv, Hkv, 2, 9000, bits, group, [9000, 1], window=window)
+
+
+def test_decode_ragged_batch():
+    """Many sequences of very different lengths: each must be seen whole, once."""
+    lens = [(37 * i * i) % 501 for i in range(60)]
+    run_decode(60, 2, 2, 1, 500, 4, 64, lens)
+
+
+def test_decode_large_scores():
+    """Scores in the hundreds: one key takes all the weight, nothing overflows."""
+    run_decode(2, 2, 1, 1, 300, 8, 64, [300, 299], scale=5.0)
+    run_decode(2, 2, 1, 1, 300, 4, 32, [300, 299], scale=1e-6)
+
+
+def test_decode_nan_reaches_only_the_rows_that_see_it():
+    B, H, Hkv, Tq, Tk = 2, 4, 2, 2, 90
+    lens = [90, 50]
+    cache = filled(B, Hkv, Tk, 4, 64, lens, 20)
+    q = randn((B, Tq, H, 128), 21).cuda()
+    good, good_lse = attn.attn_decode_kvq(q, cache, ints(lens))
+    cache.k_params[0, 0, 89] = float("nan")              # the newest key of sequence 0, head 0: only token 1 sees it
+    cache.v_params[1, 1, 10, 1] = float("nan")           # dims 64.. of a value of sequence 1, head 1
+    o, lse = attn.attn_decode_kvq(q, cache, ints(lens))
+    clean()
+    bad_o = torch.zeros_like(o, dtype=torch.bool)
+    bad_o[0, 1, 0:2] = True
+    bad_o[1, :, 2:4, 64:] = True
+    bad_l = torch.zeros_like(lse, dtype=torch.bool)
+    bad_l[0, 0:2, 1] = True
+    assert torch.equal(o.isnan(), bad_o) and torch.equal(lse.isnan(), bad_l)
+    assert torch.equal(o[~bad_o], good[~bad_o]) and torch.equal(lse[~bad_l], good_lse[~bad_l])
+
+
+def test_decode_extreme_scales():
+    """Groups whose scales differ by many orders of magnitude, and tiny and huge values."""
+    B, H, Hkv, Tk = 1, 2, 1, 120
+    k, v = randn((B, Tk, Hkv, 128), 30).cuda(), randn((B, Tk, Hkv, 128), 31).float().cuda()
+    v[..., :32] *= 1e30
+    v[..., 32:64] *= 1e-30
+    v[..., 64:96] += 1000
+    for bits in (4, 8):
+        cache = attn.kvq_cache(B, Hkv, Tk, bits, 32)
+        attn.kvq_write(cache, k, v.to(torch.bfloat16), ints([Tk]))
+        q = randn((B, 1, H, 128), 32).cuda()
+        o, lse = attn.attn_decode_kvq(q, cache, ints([Tk]))
+        clean()
+        check_decode(q, cache, [Tk], 128 ** -0.5, None, o, lse, f"extreme scales {bits}")
+
+
+def test_decode_is_repeatable_and_leaves_its_inputs():
+    q, cache, o, lse = run_decode(5, 4, 2, 1, 3000, 4, 32, [3000, 10, 1500, 2999, 64])
+    before = [t.clone() for t in cache]
+    ws = torch.full((attn.load_library().attn_decode_kvq_workspace_bytes(5, 4, 2, 1, 3000, 128),), 255,
+                    dtype=torch.uint8, device="cuda")    # NaN as fp32: its contents must not matter
+    for _ in range(3):
+        o2, lse2 = attn.attn_decode_kvq(q, cache, ints([3000, 10, 1500, 2999, 64]), workspace=ws)
+        clean()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(cache, before))
+
+
+def test_decode_workspace_and_neighbours_are_not_overrun():
+    """Outputs and workspace in the middle of larger buffers: the bytes around them stay."""
+    B, H, Hkv, Tq, Tk, lens = 2, 6, 3, 2, 5000, [4999, 700]
+    cache = filled(B, Hkv, Tk, 4, 64, lens, 40)
+    q = randn((B, Tq, H, 128), 41).cuda()
+    n = int(attn.load_library().attn_decode_kvq_workspace_bytes(B, H, Hkv, Tq, Tk, 128))
+    ws = torch.full((n + 512,), 77, dtype=torch.uint8, device="cuda")
+    ob = torch.full((q.numel() + 256,), 7.0, dtype=torch.bfloat16, device="cuda")
+    lb = torch.full((B * H * Tq + 64,), 7.0, device="cuda")
+    o, lse = ob[128:-128].view_as(q), lb[32:-32].view(B, H, Tq)
+    attn.attn_decode_kvq(q, cache, ints(lens), None, o, lse, ws[256:256 + n])
+    clean()
+    check_decode(q, cache, lens, 128 ** -0.5, None, o, lse, "middle")
+    assert (ws[:256] == 77).all() and (ws[256 + n:] == 77).all()
+    assert (ob[:128] == 7).all() and (ob[-128:] == 7).all() and (lb[:32] == 7).all() and (lb[-32:] == 7).all()
+
+
+# ---------------------------------------------------------------------------------------------- together, as used
+
+def test_prompt_then_steps():
+    """A prompt written, then token by token: prologue, write, decode. Each step against the float64 oracle on the
+    codes the cache holds, and the codes against the rows that the prologue gave."""
+    B, H, Hkv, bits, group, Tk = 3, 4, 2, 4, 32, 64
+    lens = torch.tensor([20, 7, 1], dtype=torch.int32, device="cuda")
+    P = 20                                               # left-padded prompts
+    raw_q, raw_k, v = (randn((B, P, h, 128), 50 + h + j).cuda() for j, h in enumerate((H, Hkv, Hkv)))
+    cache = poisoned(B, Hkv, Tk, bits, group)
+    _, k = attn.qk_norm_rope(raw_q, raw_k, pos_offsets=lens - P)
+    attn.kvq_write(cache, k, v, lens)
+    for step in range(4):
+        lens = lens + 1
+        rq, rk, v = (randn((B, 1, h, 128), 60 + 10 * step + j).cuda() for j, h in enumerate((H, Hkv, Hkv)))
+        q, k = attn.qk_norm_rope(rq, rk, pos_offsets=lens - 1)
+        attn.kvq_write(cache, k, v, lens)
+        o, lse = attn.attn_decode_kvq(q, cache, lens)
+        clean()
+        L = lens.tolist()
+        for b in range(B):
+            check_row(k[b, 0].cpu(), cache.k_codes[b, :, L[b] - 1], cache.k_params[b, :, L[b] - 1], bits, group, "step")
+        check_decode(q, cache, L, 128 ** -0.5, None, o, lse, f"step {step}")
+    # the bf16 decode over the cache read back: the same values up to their rounding to bf16
+    kb, vb = attn.kvq_read(cache)
+    o_b, _ = attn.attn_decode(q, kb, vb, lens)
+    clean()
+    assert (o_b.float() - o.float()).norm() <= 2.0 ** -6 * o.float().norm()
+
+
+def test_steps_captured_in_a_graph():
+    """A captured step (lengths + 1, write, decode) replayed against the same steps run one by one."""
+    B, H, Hkv, Tk = 2, 4, 2, 300
+    def state():
+        lens = ints([250, 3])
+        return lens, filled(B, Hkv, Tk, 4, 64, [250, 3], 70)
+    ks, vs, qs = (randn((5, B, 1, h, 128), 71 + h + j).cuda() for j, h in enumerate((Hkv, Hkv, H)))
+    lens, cache = state()
+    ref = []
+    for i in range(5):
+        lens += 1
+        attn.kvq_write(cache, ks[i], vs[i], lens)
+        ref.append([t.clone() for t in attn.attn_decode_kvq(qs[i], cache, lens)])
+    lens, cache = state()
+    k, v, q = ks[0].clone(), vs[0].clone(), qs[0].clone()
+    o, lse = torch.empty_like(q), torch.empty((B, H, 1), device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lens += 1
+        attn.kvq_write(cache, k, v, lens)
+        attn.attn_decode_kvq(q, cache, lens, None, o, lse)
+    for i in range(5):
+        for dst, src in ((k, ks), (v, vs), (q, qs)):
+            dst.copy_(src[i])
+        graph.replay()
+        clean()
+        assert torch.equal(o, ref[i][0]) and torch.equal(lse, ref[i][1]), f"step {i}"
+
+
+def test_calls_on_another_stream():
+    """Every call with stream=: ordered on that stream, outputs made there belong to it."""
+    B, H, Hkv, Tk = 2, 4, 2, 4000
+    k, v, q = (randn((B, n, h, 128), 80 + j).cuda() for j, (n, h) in enumerate(((Tk, Hkv), (Tk, Hkv), (1, H))))
+    lens = ints([Tk, 1234])
+    cache = attn.kvq_cache(B, Hkv, Tk)
+    attn.kvq_write(cache, k, v, ints([Tk, Tk]))
+    ref = [*attn.attn_decode_kvq(q, cache, lens), *attn.kvq_read(cache, 7, lens)]
+    side = torch.cuda.Stream()
+    cache2 = attn.kvq_cache(B, Hkv, Tk)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        attn.kvq_write(cache2, k, v, ints([Tk, Tk]), stream=side)
+        got.append([*attn.attn_decode_kvq(q, cache2, lens, stream=side), *attn.kvq_read(cache2, 7, lens, stream=side)])
+    torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")   # memory that the calls let go must not be theirs
+    clean()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(ref, g))
+
+
+def test_two_streams_at_once():
+    """Two decodes in flight, each with its own workspace (the binding's default)."""
+    a = (randn((1, 1, 8, 128), 90).cuda(), filled(1, 4, 8000, 4, 64, [8000], 91), ints([8000]))
+    b = (randn((3, 2, 4, 128), 92).cuda(), filled(3, 4, 2500, 8, 32, [2500, 9, 700], 94), ints([2500, 9, 700]))
+    ref = [attn.attn_decode_kvq(*x) for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[attn.attn_decode_kvq(*x, stream=s) for x, s in zip((a, b), streams)] for _ in range(10)]
+    clean()
+    for pair in got:
+        for r, g in zip(ref, pair):
+            assert torch.equal(r[0], g[0]) and torch.equal(r[1], g[1])
+
+
+def test_offsets_past_32_bits():
+    """A cache whose codes pass 4 GiB a tensor: the last sequence's rows are written, read and attended to."""
+    B, Hkv, Tk = 2, 2, (1 << 32) // (128 * 4) + 333       # 8-bit codes: B * Hkv * Tk * 128 bytes > 2^32
+    cache = attn.kvq_cache(B, Hkv, Tk, 8, 128)
+    lens = ints([5, Tk])
+    k, v = randn((B, 40, Hkv, 128), 95).cuda(), randn((B, 40, Hkv, 128), 96).cuda()
+    attn.kvq_write(cache, k, v, lens)
+    check_row(k[1].cpu(), cache.k_codes[1, :, Tk - 40:].transpose(0, 1), cache.k_params[1, :, Tk - 40:].transpose(0, 1),
+              8, 128, "k")
+    rk, rv = attn.kvq_read(cache, 40, lens)
+    for x, y, p in ((k, rk, cache.k_params), (v, rv, cache.v_params)):
+        step = p[1, :, Tk - 40:, :, 0].transpose(0, 1).float()
+        assert ((x[1].float() - y[1].float()).abs() <= step / 2 * 1.02 + 2.0 ** -7 * x[1].float().abs()).all()
+        assert (y[0, :35] == 0).all()
+    q = randn((B, 1, 2, 128), 97).cuda()
+    o, lse = attn.attn_decode_kvq(q, cache, lens, window=39)
+    clean()
+    tail = tuple(torch.stack([t[0, :, :40], t[1, :, Tk - 40:]]) for t in cache)
+    check_decode(q, tail, [5, 40], 128 ** -0.5, 39, o, lse, "past 32 bits")
+    del cache
+    torch.cuda.empty_cache()
