@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -257,8 +258,37 @@ attn_status check_decode(int B, int H, int Hkv, int Tq, int Tk, int D, int bits,
   if (st != ATTN_OK) return st;
   if ((H / Hkv) * static_cast<long long>(Tq) > attn::kKvqMaxRows) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H * Tq > 0x7fffffffLL / 8) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hkv > (1LL << 40) / Tk) return ATTN_ERR_UNSUPPORTED;
+  // the units' 16-key tiles are counted in 31 bits
+  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL / (Tk / attn::kKvqTile + 1)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
+}
+
+// Keys a sequence's rows can see: the whole cache, or with a sliding window the Tq + window before its end.
+int decode_span(int Tq, int Tk, int window) {
+  return window < 0 ? Tk : static_cast<int>(std::min<long long>(Tk, static_cast<long long>(Tq) + window));
+}
+
+// CTAs of the split kernel: two per SM, or fewer where every warp of a CTA would not get a tile.
+unsigned decode_grid(int B, int H, int Hkv, int Tq, int span) {
+  const int R = (H / Hkv) * Tq, n_rt = R <= 4 ? 1 : (R + 7) / 8, slices = attn::kKvqWarps / n_rt;
+  const long long tiles = static_cast<long long>(B) * Hkv * ((span + attn::kKvqTile - 1) / attn::kKvqTile);
+  return static_cast<unsigned>(std::min<long long>(attn::kKvqCtas, (tiles + slices - 1) / slices));
+}
+
+size_t decode_workspace(int B, int H, int Hkv, int Tq, int Tk) {
+  const size_t pieces = static_cast<size_t>(decode_grid(B, H, Hkv, Tq, Tk)), rows = pieces * 2 * ((H / Hkv) * Tq);
+  return pieces * sizeof(attn::KvqSpan) + rows * (128 + 2) * 4;
+}
+
+template <int kBits, int kGroup, bool kDup>
+cudaError_t launch_split(const attn::KvqDecodeParams& p, unsigned ctas, cudaStream_t s) {
+  auto kernel = attn::kvq_decode_split_kernel<kBits, kGroup, kDup>;
+  constexpr int kSmem = attn::KvqShape<kBits, kGroup, kDup>::kSmem;
+  static_assert(2 * (kSmem + 1024 + 64) <= 228 * 1024, "two CTAs per SM");
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, attn::kKvqThreads, kSmem, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -323,12 +353,12 @@ attn_status attn_kvq_read(const void* k_codes, const void* k_params, const void*
 
 size_t attn_decode_kvq_workspace_bytes(int B, int H, int H_kv, int Tq, int Tk, int D) {
   if (check_decode(B, H, H_kv, Tq, Tk, D, 4, 128, 1.0f) != ATTN_OK) return 0;
-  return 16;
+  return decode_workspace(B, H, H_kv, Tq, Tk);
 }
 
 int attn_decode_kvq_kernels(int B, int H, int H_kv, int Tq, int Tk, int D, int window) {
   if (check_decode(B, H, H_kv, Tq, Tk, D, 4, 128, 1.0f) != ATTN_OK || window < -1) return 0;
-  return 1;
+  return decode_grid(B, H, H_kv, Tq, decode_span(Tq, Tk, window)) > 1 ? 2 : 1;
 }
 
 attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
@@ -364,12 +394,34 @@ attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_pa
   p.B = B, p.H = H, p.Hkv = H_kv, p.Tq = Tq, p.Tk = Tk;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
+  const int R = p.R = (H / H_kv) * Tq;
+  const unsigned ctas = decode_grid(B, H, H_kv, Tq, decode_span(Tq, Tk, window));
+  // (laid out for the most CTAs, those without a window)
+  const size_t most = decode_grid(B, H, H_kv, Tq, Tk);
+  p.spans = static_cast<attn::KvqSpan*>(workspace);
+  p.part_o = reinterpret_cast<float*>(p.spans + most);
+  p.part_ml = p.part_o + most * 2 * R * 128;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
   with_format(bits, group, [&](auto b, auto g) {
-    attn::kvq_decode_rows_kernel<b.value, g.value><<<static_cast<unsigned>(B * H * Tq), 128, 0, s>>>(p);
+    if (R <= 4) e = launch_split<b.value, g.value, true>(p, ctas, s);
+    else e = launch_split<b.value, g.value, false>(p, ctas, s);
   });
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "kvq_decode_rows_kernel launch");
+  if (e != cudaSuccess) return cuda_fail(e, "kvq_decode_split_kernel launch");
+  if (ctas > 1) {
+    // Launched while the split kernel runs (its blocks wait for that grid's end), so that its start costs nothing.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, R);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, attn::kvq_decode_merge_kernel, p)) != cudaSuccess)
+      return cuda_fail(e, "kvq_decode_merge_kernel launch");
+  }
   return ATTN_OK;
 }
 

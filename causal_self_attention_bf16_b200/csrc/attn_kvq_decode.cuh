@@ -1,5 +1,33 @@
 // Attention of a few new queries over the quantised key/value cache (include/attn.h, attn_decode_kvq): the cached
-// decode of attn_decode with keys and values held as 4- or 8-bit codes that stand for n * s + z per group of dims.
+// decode of attn_decode with keys and values held as 4- or 8-bit codes n that stand for n * s + z per group of dims.
+//
+// The cache is read once and bounds the call: a key and its value are 2 * (16 * bits + 512 / group) bytes, 136 to
+// 160 at 4 bits, and at the 6.56 TB/s of an HBM copy an SM gets about 23 bytes per clock, a 16-key tile every 110
+// clocks. CUDA cores alone cannot turn 4,096 codes into products in that time (two operations a code are 64 clocks
+// of every lane), so the codes go to the matrix unit: as A fragments of mma.m16n8k16 (bf16 in, fp32 sums) made in
+// registers, four codes from one shift and one logical operation. tcgen05 would need them widened in shared or
+// tensor memory first, four bytes written for every byte read, to fill 128-row tiles with 1 to 32 queries.
+//
+//   Codes. bf16 16.0 is 0x4180 with a mantissa step of 1/8, so a nibble n shifted to bits 3-6 and or'ed in is the
+//   number 16 + n, exactly; with 0x4380 it is 256 + 16 n. Four nibbles of each half of a 32-bit word become four
+//   registers of two numbers, one shift and one logical operation each. An 8-bit code is its two nibbles,
+//   (16 + low) + (256 + 16 high), multiplied in turn into one sum. The offset (16, or 272) comes off again with the
+//   sums that have to be made anyhow.
+//   Scores. For key j and query row r, with the sums taken group by group of dims:
+//     q . k = sum_g s_g (sum_d q_d n_d) + z_g (sum_d q_d).     The first sum is the matrix product (its accumulator
+//   starts at -offset * sum_d q_d), the second is made once per query row. q stays bf16 as given.
+//   Values. o = sum_j p_j s_g n + sum_j p_j z_g.  p_j s_g is the B fragment, carried as the sum of two bf16 numbers
+//   (16 bits), so its rounding is 2^-17 of itself; the second sum is per group and row, in fp32, and takes the
+//   offset with it. Up to 4 rows the two halves are the two halves of the tile's 8 columns; from 5 rows on they are
+//   multiplied in turn.
+//   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 8 (then p <= 2^8
+//   and the sums stay far from overflow): one vote a tile in place of the reduction and the rescaling.
+//
+// Work split. A unit is one (sequence, key/value head); its visible keys, tiles of 16. All units' tiles in a row are
+// dealt to the CTAs in equal stretches, found on the device from the lengths, so that every CTA reads the same
+// number of bytes however ragged the batch; a CTA's warps take its tiles in turn, through a ring of tiles in shared
+// memory that each warp fills for itself (cp.async; no barrier in the loop). A unit that ends in the CTA it began in
+// is finished there; one that spans CTAs leaves unnormalised pieces, which kvq_decode_merge_kernel joins.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -12,10 +40,23 @@ namespace attn {
 // This unit's device error word (kind 2 = an address check of the debug build failed, site in the higher bits).
 __device__ uint32_t g_kvq_error;
 
-constexpr int kKvqMaxRows = 32;  // (H / H_kv) * Tq query rows per key/value head, at most
+constexpr int kKvqMaxRows = 32;   // (H / H_kv) * Tq query rows per key/value head, at most
+constexpr int kKvqWarps = 8;      // warps per CTA
+constexpr int kKvqThreads = kKvqWarps * 32;
+constexpr int kKvqCtas = 2 * 148;  // CTAs of the split kernel, at most: two per SM
+constexpr int kKvqTile = 16;      // keys per tile
 
 enum : uint32_t {
-  kSiteKvqDecQ = 0xa4, kSiteKvqDecCodes = 0xa5, kSiteKvqDecParams = 0xa6, kSiteKvqDecO = 0xa7, kSiteKvqDecLse = 0xa8
+  kSiteKvqDecQ = 0xa4, kSiteKvqDecCodes = 0xa5, kSiteKvqDecParams = 0xa6, kSiteKvqDecO = 0xa7, kSiteKvqDecLse = 0xa8,
+  kSiteKvqDecPart = 0xa9
+};
+
+// What a CTA of the split kernel leaves for the merge kernel: the unit that begins in it and goes on past it.
+struct KvqSpan {
+  int unit;      // b * H_kv + hk, or -1: none
+  int last_cta;  // the CTA it ends in
+  int slot;      // this CTA's piece of it: 0 (its first stretch) or 1 (its last)
+  int pad;
 };
 
 struct KvqDecodeParams {
@@ -27,74 +68,603 @@ struct KvqDecodeParams {
   const int* seqlens;            // [B]
   __nv_bfloat16* o;              // [B, Tq, H, 128]
   float* lse;                    // [B, H, Tq]
-  int B, H, Hkv, Tq, Tk;
+  KvqSpan* spans;                // [grid]
+  float* part_ml;                // [grid, 2, R, 2]: a piece's max (log2 units) and sum per row
+  float* part_o;                 // [grid, 2, R, 128]: its unnormalised output
+  int B, H, Hkv, Tq, Tk, R;
   int window;                    // sliding window: the query at position p sees keys p - window .. p; -1: none
   float scale_log2;              // scale * log2(e)
 };
 
-template <int kBits>
-__device__ __forceinline__ float kvq_code(const uint8_t* row, int d) {
-  if constexpr (kBits == 4) return static_cast<float>((row[d / 2] >> (4 * (d & 1))) & 15);
-  else return static_cast<float>(row[d]);
+// ------------------------------------------------------------------------------------------------ fragments
+
+// 16 keys x 16 dims (A, row-major) times 16 dims x 8 rows (B): c[0..1] = A row lane / 4, columns 2 (lane % 4) + 0..1;
+// c[2..3] = A row lane / 4 + 8.
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One CTA of 128 threads per output row (b, i, h), over its visible keys in blocks of 128: thread j scores key j,
-// the block takes its maximum (online softmax in base 2, fp32), then thread d sums dim d over the block's keys.
-template <int kBits, int kGroup>
-__global__ void __launch_bounds__(128) kvq_decode_rows_kernel(const KvqDecodeParams p) {
-  constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
-  __shared__ float qs[128], ps[128], red[4];
-  const int t = threadIdx.x;
-  const int h = blockIdx.x % p.H, i = (blockIdx.x / p.H) % p.Tq, b = blockIdx.x / p.H / p.Tq;
-  const int hk = h / (p.H / p.Hkv);
-  const int L = min(max(p.seqlens[b], 0), p.Tk);
-  const int last = L - p.Tq + i;
-  const int first = p.window < 0 ? 0 : max(0, last - p.window);
-  const size_t q_off = ((static_cast<size_t>(b) * p.Tq + i) * p.H + h) * 128 + t;
-  const size_t row0 = (static_cast<size_t>(b) * p.Hkv + hk) * p.Tk;
+// Transpose of an 8 x 8 matrix of 16-bit numbers held two to a lane.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Nibble I of each half of w as the bf16 numbers kMagic + n (in steps of kMagic / 16).
+template <int I, uint32_t kMagic>
+__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
+  uint32_t x;
+  if constexpr (I == 0) x = w << 3;
+  else x = w >> (4 * I - 3);
+  return (x & 0x00780078u) | kMagic;
+}
+constexpr uint32_t kMagic16 = 0x41804180u, kMagic256 = 0x43804380u;
+
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {  // 0 where not valid
+  const int n = valid ? kBytes : 0;
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <int kWords>
+__device__ __forceinline__ void lds(uint32_t (&w)[kWords], uint32_t addr) {
+  static_assert(kWords == 1 || kWords == 2 || kWords % 4 == 0, "32, 64 or a multiple of 128 bits");
+  if constexpr (kWords == 1) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  } else if constexpr (kWords == 2) {
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(addr + 4 * i));
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ layout
+
+// A tile in shared memory: 16 key rows of codes, 16 value rows, then 16 rows of key and of value params. Chunk c (16
+// bytes) of row r sits at chunk c ^ kvq_swizzle(r). A score tile's row g is key kvq_key(g) (rows 8-15: + 8). With
+// these two every read below, 4 to 16 bytes a lane, meets each bank once: the eight keys of a row set, and the four
+// that a half (or quarter) warp reads together, fall into different banks.
+template <int kBits>
+__device__ __forceinline__ int kvq_swizzle(int r) {
+  if constexpr (kBits == 4) return (r & 2) | ((r >> 2) & 1);
+  else return ((r & 3) << 1) | ((r >> 2) & 1);
+}
+__device__ __forceinline__ int kvq_key(int g) { return ((g >> 1) & 1) | (((g ^ (g >> 2)) & 1) << 1) | (g & 4); }
+
+template <int kBits, int kGroup, bool kDup>
+struct KvqShape {
+  static constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
+  static constexpr int kCodeBytes = kKvqTile * kRowBytes, kParamBytes = kKvqTile * kGroups * 4;
+  static constexpr int kStageBytes = 2 * kCodeBytes + 2 * kParamBytes;
+  // Tiles per warp in the ring: one in use, the others in flight (4 bits: 2-2.5 KB a tile, 8 bits: 4-4.5 KB).
+  static constexpr int kStages = kBits == 4 ? 3 : 2;
+  static constexpr int kRing = kKvqWarps * kStages * kStageBytes;
+  static constexpr int kCols = kDup ? 4 : 8;  // query rows per warp
+  static constexpr int kMerge = kKvqWarps * kCols * (128 + 2) * 4;
+  static constexpr int kSmem = kRing + kMerge;
+};
+
+// A sequence's keys that any of its queries sees, [start, L), and how many tiles they are.
+struct KvqSeq {
+  int L, start, tiles;
+};
+__device__ __forceinline__ KvqSeq kvq_seq(const KvqDecodeParams& p, int b) {
+  KvqSeq s;
+  s.L = min(max(p.seqlens[b], 0), p.Tk);  // lengths outside [0, Tk] are clamped
+  s.start = p.window < 0 ? 0 : max(0, s.L - p.Tq - p.window);
+  s.tiles = (s.L - s.start + kKvqTile - 1) / kKvqTile;
+  return s;
+}
+
+// A place in the row of all units' tiles.
+struct KvqCursor {
+  int b, hk, tile;
+  KvqSeq s;
+};
+__device__ __forceinline__ void kvq_next_unit(const KvqDecodeParams& p, KvqCursor& c) {
+  if (++c.hk < p.Hkv) return;
+  c.hk = 0;
+  do {
+    if (++c.b >= p.B) {
+      c.s.tiles = 0x7fffffff;  // (past the last unit: never asked for)
+      return;
+    }
+    c.s = kvq_seq(p, c.b);
+  } while (c.s.tiles == 0);
+}
+
+// ------------------------------------------------------------------------------------------------ split kernel
+
+// kDup: up to 4 query rows per key/value head, in columns 0-3 and again in 4-7; otherwise warps take up to 8 rows
+// each (n_rt = ceil(R / 8) row tiles) and kKvqWarps / n_rt share the keys.
+template <int kBits, int kGroup, bool kDup>
+__global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const KvqDecodeParams p) {
+  using Shape = KvqShape<kBits, kGroup, kDup>;
+  constexpr int kGroups = Shape::kGroups, kRowBytes = Shape::kRowBytes, kStages = Shape::kStages, kCols = Shape::kCols;
+  constexpr int kWords = kGroup * kBits / 128;       // 32-bit words of a key row and group that a lane scores
+  constexpr int kVWords = kGroup * kBits / 256;      // words of a value row and group that a lane multiplies (or 0: half)
+  constexpr float kOffset = kBits == 4 ? 16.f : 272.f;
+  constexpr float kNone = -3e38f;                    // running max before the first key
+  extern __shared__ __align__(16) uint8_t kvq_smem[];
+  __shared__ int sh_scan[kKvqWarps];
+  __shared__ int sh_b, sh_off;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int R = p.R, G = p.H / p.Hkv;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge kernel waits for this grid's end)
+
+  // Every sequence's tile count, summed: thread i takes sequences [i per, (i + 1) per).
+  const int per = (p.B + kKvqThreads - 1) / kKvqThreads;
+  int sum = 0;
+  for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) sum += kvq_seq(p, b).tiles;
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) sh_scan[warp] = incl;
+  __syncthreads();
+  int before = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kKvqWarps; ++w) {
+    if (w < warp) before += sh_scan[w];
+    total += sh_scan[w];
+  }
+  total *= p.Hkv;
+  const int n_rt = kDup ? 1 : (R + 7) / 8;
+  const int slices = kKvqWarps / n_rt;                  // warps that share the keys
+  const int share = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), slices);
+  const long long first64 = static_cast<long long>(blockIdx.x) * share;
+  const int first = first64 < total ? static_cast<int>(first64) : total;
+  const int last = static_cast<int>(min(static_cast<long long>(total), first64 + share));  // this CTA's tiles
+  if (first < last && before * p.Hkv <= first && first < (before + sum) * p.Hkv) {
+    int b = tid * per, at = before * p.Hkv;
+    for (;; ++b) {
+      const int n = kvq_seq(p, b).tiles * p.Hkv;
+      if (first < at + n) break;
+      at += n;
+    }
+    sh_b = b;
+    sh_off = first - at;
+  }
+  // Sequences without keys: o = 0, lse = -inf, shared out over the CTAs.
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (kvq_seq(p, b).tiles > 0) continue;
+    uint4* o4 = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(b) * p.Tq * p.H * 128);
+    for (int i = tid; i < p.Tq * p.H * 16; i += kKvqThreads) o4[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < p.Tq * p.H; i += kKvqThreads) p.lse[static_cast<size_t>(b) * p.Tq * p.H + i] = -INFINITY;
+  }
+  if (first >= last) {
+    if (tid == 0) p.spans[blockIdx.x].unit = -1;
+    return;
+  }
+  __syncthreads();
+
+  KvqCursor cur;  // the unit being computed
+  cur.b = sh_b;
+  cur.s = kvq_seq(p, cur.b);
+  cur.hk = sh_off / cur.s.tiles;
+  cur.tile = sh_off % cur.s.tiles;
+  const int rt = kDup ? 0 : warp % n_rt, slice = kDup ? warp : warp / n_rt;
+  const bool active = slice < slices;  // (three row tiles leave two warps over)
+
+  // --- the ring
+  const uint32_t ring = sm100::smem_u32(kvq_smem) + warp * kStages * Shape::kStageBytes;
+  KvqCursor pre = cur;  // the next tile this warp fetches
+  pre.tile += slice;
+  int pre_lin = first + slice;
+  auto settle = [&]() {
+    while (pre.tile >= pre.s.tiles) {
+      pre.tile -= pre.s.tiles;
+      kvq_next_unit(p, pre);
+    }
+  };
   const size_t n_rows = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_rows;
-  qs[t] = ATTN_IN_RANGE(q_off, 1, static_cast<size_t>(p.B) * p.Tq * p.H * 128, kSiteKvqDecQ, &g_kvq_error)
-              ? __bfloat162float(p.q[q_off]) * p.scale_log2 : 0.f;
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int kb = first; kb <= last; kb += 128) {
-    const int n = min(128, last + 1 - kb);
-    float s = -INFINITY;
-    if (t < n && ATTN_IN_RANGE(row0 + kb + t, 1, n_rows, kSiteKvqDecCodes, &g_kvq_error)) {
-      const uint8_t* c = p.k_codes + (row0 + kb + t) * kRowBytes;
-      const uint32_t* w = p.k_params + (row0 + kb + t) * kGroups;
-      s = 0.f;
-      for (int g = 0; g < kGroups; ++g) {
-        const float sc = __uint_as_float(w[g] << 16), z = __uint_as_float(w[g] & 0xffff0000u);
-        for (int d = g * kGroup; d < (g + 1) * kGroup; ++d) s = fmaf(qs[d], fmaf(kvq_code<kBits>(c, d), sc, z), s);
+  auto fetch = [&](int stage) {  // copies (or nothing) and one commit
+    if (active && pre_lin < last) {
+      settle();
+      const int key0 = pre.s.start + pre.tile * kKvqTile, n = pre.s.L - key0;  // valid rows: n >= 1
+      const size_t row0 = (static_cast<size_t>(pre.b) * p.Hkv + pre.hk) * p.Tk + key0;
+      const uint32_t to = ring + stage * Shape::kStageBytes;
+      constexpr int kChunks = kRowBytes / 16;  // per row
+#pragma unroll
+      for (int i = 0; i < kKvqTile * kChunks / 32; ++i) {
+        const int r = lane / kChunks + i * (32 / kChunks), c = lane % kChunks;
+        const bool in = r < n && ATTN_IN_RANGE(row0 + r, 1, n_rows, kSiteKvqDecCodes, &g_kvq_error);
+        const size_t from = in ? (row0 + r) * kRowBytes + c * 16 : 0;
+        const uint32_t at = to + r * kRowBytes + ((c ^ kvq_swizzle<kBits>(r)) << 4);
+        cp_async<16>(at, p.k_codes + from, in);
+        cp_async<16>(at + Shape::kCodeBytes, p.v_codes + from, in);
+      }
+      const int r = lane % 16;
+      const bool in = r < n && ATTN_IN_RANGE(row0 + r, 1, n_rows, kSiteKvqDecParams, &g_kvq_error);
+      cp_async<kGroups * 4>(to + 2 * Shape::kCodeBytes + lane * kGroups * 4,
+                            (lane < 16 ? p.k_params : p.v_params) + (in ? (row0 + r) * kGroups : 0), in);
+      pre_lin += slices;
+      pre.tile += slices;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+
+  float* mg_o = reinterpret_cast<float*>(kvq_smem + Shape::kRing);        // [warp][column][128]
+  float* mg_ml = mg_o + kKvqWarps * kCols * 128;                         // [warp][column][2]
+  const size_t n_q = static_cast<size_t>(p.B) * p.Tq * p.H * 128;
+  (void)n_q;
+
+  int stage = 0, lin = first;  // lin: first tile of the current piece
+  int mine = first + slice;    // this warp's next tile
+  while (lin < last) {
+    // --- one piece: tiles [lin, piece_end) of unit (cur.b, cur.hk), from its tile cur.tile on
+    const int piece_end = min(last, lin + cur.s.tiles - cur.tile);
+    const bool whole = cur.tile == 0 && piece_end - lin == cur.s.tiles;
+    // The unit's queries as B fragments: column g is row `row`; the lane holds its dims that meet word w of group j
+    // of a key row, paired as the codes' nibbles are.
+    const int row = kDup ? (g & 3) : rt * 8 + g;
+    uint32_t qb[16];
+    float qsum[kGroups][2];  // per group, the sum of q over its dims, of columns 2 t and 2 t + 1
+    {
+      const int i = row % p.Tq, h = cur.hk * G + row / p.Tq;
+      const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128;
+      const bool live = row < R && ATTN_IN_RANGE(off, 128, n_q, kSiteKvqDecQ, &g_kvq_error);
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        float part = 0.f;
+#pragma unroll
+        for (int e = 0; e < kGroup / 32; ++e) {  // 8 dims at a time
+          const int x = j * (kGroup / 32) + e;
+          uint4 u = make_uint4(0u, 0u, 0u, 0u);
+          if (live) u = *reinterpret_cast<const uint4*>(p.q + off + j * kGroup + t * (kGroup / 4) + 8 * e);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) part += __uint_as_float(w[y] << 16) + __uint_as_float(w[y] & 0xffff0000u);
+          if constexpr (kBits == 4) {  // dims (0,4) (1,5) (2,6) (3,7) of a word's eight
+            qb[4 * x] = __byte_perm(w[0], w[2], 0x5410);
+            qb[4 * x + 1] = __byte_perm(w[0], w[2], 0x7632);
+            qb[4 * x + 2] = __byte_perm(w[1], w[3], 0x5410);
+            qb[4 * x + 3] = __byte_perm(w[1], w[3], 0x7632);
+          } else {  // dims (0,2) (1,3) of each word's four
+            qb[4 * x] = __byte_perm(w[0], w[1], 0x5410);
+            qb[4 * x + 1] = __byte_perm(w[0], w[1], 0x7632);
+            qb[4 * x + 2] = __byte_perm(w[2], w[3], 0x5410);
+            qb[4 * x + 3] = __byte_perm(w[2], w[3], 0x7632);
+          }
+        }
+        part += __shfl_xor_sync(0xffffffffu, part, 1);
+        part += __shfl_xor_sync(0xffffffffu, part, 2);
+        qsum[j][0] = __shfl_sync(0xffffffffu, part, 8 * t);
+        qsum[j][1] = __shfl_sync(0xffffffffu, part, 8 * t + 4);
       }
     }
-    float mx = s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (t % 32 == 0) red[t / 32] = mx;
-    __syncthreads();
-    const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float a = m == m_new ? 1.f : exp2f(m - m_new);
-    ps[t] = s == -INFINITY ? 0.f : exp2f(s - m_new);  // (a NaN score makes its row NaN)
-    __syncthreads();
-    acc *= a, l *= a, m = m_new;
-    for (int j = 0; j < n; ++j) {
-      if (!ATTN_IN_RANGE(row0 + kb + j, 1, n_rows, kSiteKvqDecCodes, &g_kvq_error)) break;
-      const uint32_t w = p.v_params[(row0 + kb + j) * kGroups + t / kGroup];
-      const float v = fmaf(kvq_code<kBits>(p.v_codes + (row0 + kb + j) * kRowBytes, t), __uint_as_float(w << 16),
-                           __uint_as_float(w & 0xffff0000u));
-      acc = fmaf(ps[j], v, acc);
-      l += ps[j];
+    // Keys that columns 2 t and 2 t + 1 see: [see_lo, see_hi].
+    int see_lo[2], see_hi[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int col = 2 * t + c, r = kDup ? (col & 3) : rt * 8 + col;
+      see_hi[c] = cur.s.L - p.Tq + r % p.Tq;
+      see_lo[c] = p.window < 0 ? 0 : see_hi[c] - p.window;
+    }
+    float acc[8][4], corr[kGroups][2], m[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = 0.f;
+
+    for (; active && mine < piece_end; mine += slices) {
+      const int key0 = cur.s.start + (cur.tile + mine - lin) * kKvqTile;
+      cp_async_wait<kStages - 2>();
+      __syncwarp();  // this tile is in, and every lane has read the one before it
+      fetch(stage == 0 ? kStages - 1 : stage - 1);
+      const uint32_t at = ring + stage * Shape::kStageBytes;
+      const uint32_t kp_at = at + 2 * Shape::kCodeBytes, vp_at = kp_at + Shape::kParamBytes;
+      const int kg = kvq_key(g);
+      // --- scores: rows g and g + 8 are keys kg and kg + 8
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        uint32_t sz[2][kGroups];
+        lds(sz[0], kp_at + kg * kGroups * 4);
+        lds(sz[1], kp_at + (kg + 8) * kGroups * 4);
+        const uint32_t row_at = at + kg * kRowBytes;
+        const int sw = kvq_swizzle<kBits>(kg);  // (the same for kg + 8)
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+          float c[4];
+          c[0] = c[2] = -kOffset * qsum[j][0];
+          c[1] = c[3] = -kOffset * qsum[j][1];
+          constexpr int kPart = kWords < 4 ? kWords : 4;  // words read at once
+#pragma unroll
+          for (int w0 = 0; w0 < kWords; w0 += kPart) {
+            const int byte = j * (kGroup * kBits / 8) + t * kWords * 4 + w0 * 4;
+            const uint32_t a = row_at + (((byte >> 4) ^ sw) << 4) + (byte & 15);
+            uint32_t ka[kPart], kb[kPart];
+            lds(ka, a);
+            lds(kb, a + 8 * kRowBytes);
+#pragma unroll
+            for (int w = 0; w < kPart; ++w) {
+              if constexpr (kBits == 4) {
+                const uint32_t* b = qb + 4 * (j * kWords + w0 + w);
+                mma_16x8x16(c, nibbles<0, kMagic16>(ka[w]), nibbles<0, kMagic16>(kb[w]), nibbles<1, kMagic16>(ka[w]),
+                            nibbles<1, kMagic16>(kb[w]), b[0], b[1]);
+                mma_16x8x16(c, nibbles<2, kMagic16>(ka[w]), nibbles<2, kMagic16>(kb[w]), nibbles<3, kMagic16>(ka[w]),
+                            nibbles<3, kMagic16>(kb[w]), b[2], b[3]);
+              } else {
+                const uint32_t* b = qb + 2 * (j * kWords + w0 + w);
+                mma_16x8x16(c, nibbles<0, kMagic16>(ka[w]), nibbles<0, kMagic16>(kb[w]), nibbles<2, kMagic16>(ka[w]),
+                            nibbles<2, kMagic16>(kb[w]), b[0], b[1]);
+                mma_16x8x16(c, nibbles<1, kMagic256>(ka[w]), nibbles<1, kMagic256>(kb[w]), nibbles<3, kMagic256>(ka[w]),
+                            nibbles<3, kMagic256>(kb[w]), b[0], b[1]);
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[e] = fmaf(__uint_as_float(sz[e / 2][j] << 16), c[e],
+                        fmaf(__uint_as_float(sz[e / 2][j] & 0xffff0000u), qsum[j][e & 1], s[e]));
+        }
+      }
+      // --- softmax: keys past a row's last (or before its window) have weight 0, whatever they hold
+      const bool all_seen = key0 + kKvqTile - 1 <= cur.s.L - p.Tq && (p.window < 0 || key0 >= cur.s.L - 1 - p.window);
+      bool seen[4] = {true, true, true, true};
+      if (!all_seen) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + kg + 8 * (e / 2);
+          seen[e] = key >= see_lo[e & 1] && key <= see_hi[e & 1];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = seen[e] ? s[e] * p.scale_log2 : -INFINITY;
+      const bool raise = s[0] > m[0] + 8.f || s[2] > m[0] + 8.f || s[1] > m[1] + 8.f || s[3] > m[1] + 8.f;
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = fmaxf(fmaxf(s[c], s[c + 2]), m[c]);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+          const float f = ex2(m[c] - x);
+          m[c] = x;
+          l[c] *= f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i][c] *= f, acc[i][c + 2] *= f;
+#pragma unroll
+          for (int j = 0; j < kGroups; ++j) corr[j][c] *= f;
+        }
+      }
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pr[e] = ex2(s[e] - m[e & 1]);
+      l[0] += pr[0] + pr[2];
+      l[1] += pr[1] + pr[3];
+      // --- values
+      {
+        uint32_t sz[2][kGroups];
+        lds(sz[0], vp_at + kg * kGroups * 4);
+        lds(sz[1], vp_at + (kg + 8) * kGroups * 4);
+        // the lane's four keys of a value tile: A fragment columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        const int k0 = kvq_key(2 * t), k1 = kvq_key(2 * t + 1);
+        const uint32_t v_at = at + Shape::kCodeBytes;
+        const int sw0 = kvq_swizzle<kBits>(k0), sw1 = kvq_swizzle<kBits>(k1);
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+          uint32_t hi[2], lo[2];  // p s of keys kg (+ 8) and columns 2 t, 2 t + 1, in two bf16 parts
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float sc = __uint_as_float(sz[y][j] << 16), z = __uint_as_float(sz[y][j] & 0xffff0000u);
+            const float zo = fmaf(-kOffset, sc, z);
+            float v0 = pr[2 * y] * sc, v1 = pr[2 * y + 1] * sc;
+            float d0 = pr[2 * y] * zo, d1 = pr[2 * y + 1] * zo;
+            if (!all_seen) {  // (a NaN in a key that a row does not see stays out of it)
+              v0 = seen[2 * y] ? v0 : 0.f, v1 = seen[2 * y + 1] ? v1 : 0.f;
+              d0 = seen[2 * y] ? d0 : 0.f, d1 = seen[2 * y + 1] ? d1 : 0.f;
+            }
+            corr[j][0] += d0;
+            corr[j][1] += d1;
+            const uint32_t h = sm100::pack_bf16x2(v0, v1);
+            const uint32_t e = sm100::pack_bf16x2(v0 - __uint_as_float(h << 16), v1 - __uint_as_float(h & 0xffff0000u));
+            if constexpr (kDup) {
+              hi[y] = movmatrix(t < 2 ? h : e);
+            } else {
+              hi[y] = movmatrix(h);
+              lo[y] = movmatrix(e);
+            }
+          }
+          auto mul = [&](float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            mma_16x8x16(c, a0, a1, a2, a3, hi[0], hi[1]);
+            if constexpr (!kDup) mma_16x8x16(c, a0, a1, a2, a3, lo[0], lo[1]);
+          };
+          // Words w of the lane's dims j * kGroup + g * (kGroup / 8) + ...: eight (4 bits) or four (8 bits) dims of
+          // each key; with 4 bits and groups of 32 the lane's four dims are half a word.
+          constexpr int kRead = kVWords < 1 ? 1 : kVWords;
+          const int byte = j * (kGroup * kBits / 8) + (kVWords < 1 ? (g >> 1) * 4 : g * kVWords * 4);
+          uint32_t va[kRead], vb[kRead], vc[kRead], vd[kRead];
+          const uint32_t a0 = v_at + k0 * kRowBytes + (((byte >> 4) ^ sw0) << 4) + (byte & 15);
+          const uint32_t a1 = v_at + k1 * kRowBytes + (((byte >> 4) ^ sw1) << 4) + (byte & 15);
+          lds(va, a0);
+          lds(vb, a1);
+          lds(vc, a0 + 8 * kRowBytes);
+          lds(vd, a1 + 8 * kRowBytes);
+          constexpr int kTiles = kGroup / 16;  // tiles of 16 dims in the group
+          if constexpr (kBits == 4) {
+#pragma unroll
+            for (int r = 0; r < kGroup / 32; ++r) {  // four dims at a time: half a word of each key
+              const uint32_t sel = kVWords < 1 ? ((g & 1) ? 0x7632u : 0x5410u) : ((r & 1) ? 0x7632u : 0x5410u);
+              const uint32_t x = __byte_perm(va[r / 2], vb[r / 2], sel), y = __byte_perm(vc[r / 2], vd[r / 2], sel);
+              mul(acc[j * kTiles + 2 * r], nibbles<0, kMagic16>(x), nibbles<1, kMagic16>(x), nibbles<0, kMagic16>(y),
+                  nibbles<1, kMagic16>(y));
+              mul(acc[j * kTiles + 2 * r + 1], nibbles<2, kMagic16>(x), nibbles<3, kMagic16>(x),
+                  nibbles<2, kMagic16>(y), nibbles<3, kMagic16>(y));
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < kGroup / 32; ++r) {  // four dims: a word of each key
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = h ? 0x7632u : 0x5410u;
+                const uint32_t x = __byte_perm(va[r], vb[r], sel), y = __byte_perm(vc[r], vd[r], sel);
+                mul(acc[j * kTiles + 2 * r + h], nibbles<0, kMagic16>(x), nibbles<2, kMagic16>(x),
+                    nibbles<0, kMagic16>(y), nibbles<2, kMagic16>(y));
+                mul(acc[j * kTiles + 2 * r + h], nibbles<1, kMagic256>(x), nibbles<3, kMagic256>(x),
+                    nibbles<1, kMagic256>(y), nibbles<3, kMagic256>(y));
+              }
+            }
+          }
+        }
+      }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+
+    // --- the piece's result: the warps' parts, joined by their maxima
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) corr[j][c] += __shfl_xor_sync(0xffffffffu, corr[j][c], o);
+      }
+    }
+    __syncthreads();  // the previous piece's parts have been read
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = i / (kGroup / 16), dim = j * kGroup + g * (kGroup / 8) + 2 * (i % (kGroup / 16));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = acc[i][c], y = acc[i][c + 2];
+        if constexpr (kDup) {
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          y += __shfl_xor_sync(0xffffffffu, y, 2);
+        }
+        if (!kDup || t < 2)
+          *reinterpret_cast<float2*>(mg_o + (warp * kCols + 2 * t + c) * 128 + dim) =
+              make_float2(x + corr[j][c], y + corr[j][c]);
+      }
+    }
+    if (g == 0 && (!kDup || t < 2)) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<float2*>(mg_ml + (warp * kCols + 2 * t + c) * 2) = make_float2(m[c], l[c]);
     }
     __syncthreads();
+    const int slot = lin == first ? 0 : 1;
+    for (int e = tid; e < R * 32; e += kKvqThreads) {
+      const int r = e / 32, d = (e % 32) * 4;
+      const int w0 = kDup ? 0 : r / 8, col = kDup ? r : r % 8, step = kDup ? 1 : n_rt;
+      float M = kNone;
+      for (int s = 0; s < slices; ++s) M = fmaxf(M, mg_ml[((w0 + s * step) * kCols + col) * 2]);
+      float L = 0.f;
+      float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < slices; ++s) {
+        const int at = (w0 + s * step) * kCols + col;
+        const float f = ex2(mg_ml[at * 2] - M);
+        L = fmaf(mg_ml[at * 2 + 1], f, L);
+        const float4 x = *reinterpret_cast<const float4*>(mg_o + at * 128 + d);
+        o4.x = fmaf(x.x, f, o4.x), o4.y = fmaf(x.y, f, o4.y), o4.z = fmaf(x.z, f, o4.z), o4.w = fmaf(x.w, f, o4.w);
+      }
+      if (whole) {
+        const int i = r % p.Tq, h = cur.hk * G + r / p.Tq;
+        const float inv = L == 0.f ? 0.f : 1.f / L;  // (a row that sees no key: 0)
+        const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128 + d;
+        if (ATTN_IN_RANGE(off, 4, n_q, kSiteKvqDecO, &g_kvq_error))
+          *reinterpret_cast<uint2*>(p.o + off) =
+              make_uint2(sm100::pack_bf16x2(o4.x * inv, o4.y * inv), sm100::pack_bf16x2(o4.z * inv, o4.w * inv));
+        const size_t lse_i = (static_cast<size_t>(cur.b) * p.H + h) * p.Tq + i;
+        if (d == 0 && ATTN_IN_RANGE(lse_i, 1, n_q / 128, kSiteKvqDecLse, &g_kvq_error))
+          p.lse[lse_i] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+      } else {
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + slot) * R + r;
+        if (ATTN_IN_RANGE(part, 1, static_cast<size_t>(gridDim.x) * 2 * R, kSiteKvqDecPart, &g_kvq_error)) {
+          *reinterpret_cast<float4*>(p.part_o + part * 128 + d) = o4;
+          if (d == 0) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(M, L);
+        }
+      }
+    }
+    if (piece_end == last && tid == 0) {  // the last piece: does its unit begin here and go on?
+      const int end = lin - cur.tile + cur.s.tiles;  // the unit's end in the row of all tiles
+      const bool on = end > last && lin - cur.tile >= first;
+      p.spans[blockIdx.x] = KvqSpan{on ? cur.b * p.Hkv + cur.hk : -1, (end - 1) / share, slot, 0};
+    }
+    lin = piece_end;
+    cur.tile = 0;
+    if (lin < last) kvq_next_unit(p, cur);
   }
-  const size_t n_out = static_cast<size_t>(p.B) * p.H * p.Tq;
-  if (ATTN_IN_RANGE(q_off, 1, n_out * 128, kSiteKvqDecO, &g_kvq_error))
-    p.o[q_off] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
+  cp_async_wait<0>();
+}
+
+// ------------------------------------------------------------------------------------------------ merge kernel
+
+// Block (x, r): row r of the unit that begins in the split kernel's CTA x and goes on past it, if there is one:
+// O = sum_s O_s 2^(m_s - M) / sum_s l_s 2^(m_s - M) over its pieces, M = max_s m_s. The pieces are shared by the
+// block's warps, a lane taking four dims, and the warps' sums are added in order.
+__global__ void __launch_bounds__(256) kvq_decode_merge_kernel(const KvqDecodeParams p) {
+  __shared__ float sh_max[8], sh_sum[8];
+  __shared__ float4 sh_o[8][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's results
+  const int x = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32, R = p.R;
+  const KvqSpan span = p.spans[x];
+  if (span.unit < 0) return;
+  const int n = span.last_cta - x + 1;  // pieces: this CTA's slot, then the first slot of each CTA after it
+  if (!ATTN_IN_RANGE(span.last_cta, 1, gridDim.x, kSiteKvqDecPart, &g_kvq_error)) return;
+  auto part = [&](int s) { return (static_cast<size_t>(x + s) * 2 + (s == 0 ? span.slot : 0)) * R + r; };
+  float M = -INFINITY;
+  for (int s = tid; s < n; s += 256) M = fmaxf(M, p.part_ml[part(s) * 2]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) sh_max[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) M = fmaxf(M, sh_max[w]);
+  float l = 0.f;
+  float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = warp; s < n; s += 8) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part(s) * 2);
+    const float4 v = reinterpret_cast<const float4*>(p.part_o + part(s) * 128)[lane];
+    const float f = ex2(ml.x - M);
+    l = fmaf(ml.y, f, l);
+    o4.x = fmaf(v.x, f, o4.x), o4.y = fmaf(v.y, f, o4.y), o4.z = fmaf(v.z, f, o4.z), o4.w = fmaf(v.w, f, o4.w);
+  }
+  sh_o[warp][lane] = o4;
+  if (lane == 0) sh_sum[warp] = l;
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) {
+    const float4 v = sh_o[w][lane];
+    o4.x += v.x, o4.y += v.y, o4.z += v.z, o4.w += v.w;
+    l += sh_sum[w];
+  }
+  const int b = span.unit / p.Hkv, hk = span.unit % p.Hkv, i = r % p.Tq, h = hk * (p.H / p.Hkv) + r / p.Tq;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t n_out = static_cast<size_t>(p.B) * p.Tq * p.H;
+  (void)n_out;
+  const size_t off = (static_cast<size_t>(b) * p.Tq + i) * p.H + h;
+  if (ATTN_IN_RANGE(off, 1, n_out, kSiteKvqDecO, &g_kvq_error))
+    reinterpret_cast<uint2*>(p.o + off * 128)[lane] =
+        make_uint2(sm100::pack_bf16x2(o4.x * inv, o4.y * inv), sm100::pack_bf16x2(o4.z * inv, o4.w * inv));
   const size_t lse_i = (static_cast<size_t>(b) * p.H + h) * p.Tq + i;
-  if (t == 0 && ATTN_IN_RANGE(lse_i, 1, n_out, kSiteKvqDecLse, &g_kvq_error))
-    p.lse[lse_i] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  if (lane == 0 && ATTN_IN_RANGE(lse_i, 1, n_out, kSiteKvqDecLse, &g_kvq_error))
+    p.lse[lse_i] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace attn
