@@ -270,7 +270,7 @@ int decode_span(int Tq, int Tk, int window) {
 
 // CTAs of the split kernel: two per SM, or fewer where every warp of a CTA would not get a tile.
 unsigned decode_grid(int B, int H, int Hkv, int Tq, int span) {
-  const int R = (H / Hkv) * Tq, n_rt = R <= 4 ? 1 : (R + 7) / 8, slices = attn::kKvqWarps / n_rt;
+  const int R = (H / Hkv) * Tq, n_rt = (R + 7) / 8, slices = attn::kKvqWarps / n_rt;
   const long long tiles = static_cast<long long>(B) * Hkv * ((span + attn::kKvqTile - 1) / attn::kKvqTile);
   return static_cast<unsigned>(std::min<long long>(attn::kKvqCtas, (tiles + slices - 1) / slices));
 }
@@ -280,10 +280,10 @@ size_t decode_workspace(int B, int H, int Hkv, int Tq, int Tk) {
   return pieces * sizeof(attn::KvqSpan) + rows * (128 + 2) * 4;
 }
 
-template <int kBits, int kGroup, bool kDup>
+template <int kBits, int kGroup>
 cudaError_t launch_split(const attn::KvqDecodeParams& p, unsigned ctas, cudaStream_t s) {
-  auto kernel = attn::kvq_decode_split_kernel<kBits, kGroup, kDup>;
-  constexpr int kSmem = attn::KvqShape<kBits, kGroup, kDup>::kSmem;
+  auto kernel = attn::kvq_decode_split_kernel<kBits, kGroup>;
+  constexpr int kSmem = attn::KvqShape<kBits, kGroup>::kSmem;
   static_assert(2 * (kSmem + 1024 + 64) <= 228 * 1024, "two CTAs per SM");
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
@@ -404,8 +404,7 @@ attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_pa
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   with_format(bits, group, [&](auto b, auto g) {
-    if (R <= 4) e = launch_split<b.value, g.value, true>(p, ctas, s);
-    else e = launch_split<b.value, g.value, false>(p, ctas, s);
+    e = launch_split<b.value, g.value>(p, ctas, s);
   });
   if (e != cudaSuccess) return cuda_fail(e, "kvq_decode_split_kernel launch");
   if (ctas > 1) {

@@ -2,24 +2,26 @@
 // decode of attn_decode with keys and values held as 4- or 8-bit codes n that stand for n * s + z per group of dims.
 //
 // The cache is read once and bounds the call: a key and its value are 2 * (16 * bits + 512 / group) bytes, 136 to
-// 160 at 4 bits, and at the 6.56 TB/s of an HBM copy an SM gets about 23 bytes per clock, a 16-key tile every 110
+// 160 at 4 bits, and at the 6.56 TB/s of an HBM copy an SM gets about 23 bytes per clock, a 16-key tile every 105
 // clocks. CUDA cores alone cannot turn 4,096 codes into products in that time (two operations a code are 64 clocks
-// of every lane), so the codes go to the matrix unit: as A fragments of mma.m16n8k16 (bf16 in, fp32 sums) made in
-// registers, four codes from one shift and one logical operation. tcgen05 would need them widened in shared or
-// tensor memory first, four bytes written for every byte read, to fill 128-row tiles with 1 to 32 queries.
+// of every lane), so the codes go to the matrix unit, as A fragments of mma.m16n8k16 (fp16 in, fp32 sums) made in
+// registers. tcgen05 would need them widened in shared or tensor memory first, four bytes written for every byte
+// read, to fill 128-row tiles with 1 to 32 queries. What bounds the loop is the widening itself, so it is kept to
+// few operations, spread over the integer and the floating-point pipe:
 //
-//   Codes. bf16 16.0 is 0x4180 with a mantissa step of 1/8, so a nibble n shifted to bits 3-6 and or'ed in is the
-//   number 16 + n, exactly; with 0x4380 it is 256 + 16 n. Four nibbles of each half of a 32-bit word become four
-//   registers of two numbers, one shift and one logical operation each. An 8-bit code is its two nibbles,
-//   (16 + low) + (256 + 16 high), multiplied in turn into one sum. The offset (16, or 272) comes off again with the
-//   sums that have to be made anyhow.
-//   Scores. For key j and query row r, with the sums taken group by group of dims:
-//     q . k = sum_g s_g (sum_d q_d n_d) + z_g (sum_d q_d).     The first sum is the matrix product (its accumulator
-//   starts at -offset * sum_d q_d), the second is made once per query row. q stays bf16 as given.
-//   Values. o = sum_j p_j s_g n + sum_j p_j z_g.  p_j s_g is the B fragment, carried as the sum of two bf16 numbers
-//   (16 bits), so its rounding is 2^-17 of itself; the second sum is per group and row, in fp32, and takes the
-//   offset with it. Up to 4 rows the two halves are the two halves of the tile's 8 columns; from 5 rows on they are
-//   multiplied in turn.
+//   Codes. In fp16, 0x6400 | n is 1024 + n for n up to 1023 and 0x5400 | n << 4 is 64 + n for n up to 15, exactly. So
+//   two of the four nibbles of a 16-bit half need no shift at all and the other two share one, and one logical
+//   operation makes a pair of them numbers; 8-bit codes take one byte permutation a pair. One packed addition then
+//   centres them, n - 8 or n - 128, exactly: small sums of both signs, which cost the fp32 accumulators little.
+//   Scores. For key j and query row r, with c the centre and the sums taken group by group of dims:
+//     q . k = sum_g s_g (sum_d q_d (n_d - c)) + (z_g + c s_g) (sum_d q_d).   The first sum is the matrix product, the
+//   last is made once per query row. A query row is scaled by a power of two that puts its largest dim into
+//   [2^10, 2^11), so that its bf16 numbers are fp16 numbers (exactly down to 2^-24, 2^-34 of the largest), and the
+//   power is taken off with the softmax scale.
+//   Values. o = sum_j p_j s_g (n - c) + sum_j p_j (z_g + c s_g). p_j s_g is the B fragment, rounded to fp16: 2^-11 of
+//   itself at most against the output's own 2^-8. So that it is in fp16's range whatever the scales, it is carried in
+//   units of a power of two per group of dims, raised when a key's scale passes it by 2^5 (and the sums rescaled). The
+//   second sum is fp32 throughout.
 //   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 8 (then p <= 2^8
 //   and the sums stay far from overflow): one vote a tile in place of the reduction and the rescaling.
 //
@@ -30,8 +32,10 @@
 // is finished there; one that spans CTAs leaves unnormalised pieces, which kvq_decode_merge_kernel joins.
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "sm100.cuh"
 
@@ -78,11 +82,11 @@ struct KvqDecodeParams {
 
 // ------------------------------------------------------------------------------------------------ fragments
 
-// 16 keys x 16 dims (A, row-major) times 16 dims x 8 rows (B): c[0..1] = A row lane / 4, columns 2 (lane % 4) + 0..1;
-// c[2..3] = A row lane / 4 + 8.
+// c += 16 x 16 (A, row-major) times 16 x 8 (B): c[0..1] = A row lane / 4, columns 2 (lane % 4) + 0..1; c[2..3] = A row
+// lane / 4 + 8.
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -100,16 +104,37 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Nibble I of each half of w as the bf16 numbers kMagic + n (in steps of kMagic / 16).
-template <int I, uint32_t kMagic>
-__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
-  uint32_t x;
-  if constexpr (I == 0) x = w << 3;
-  else x = w >> (4 * I - 3);
-  return (x & 0x00780078u) | kMagic;
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-constexpr uint32_t kMagic16 = 0x41804180u, kMagic256 = 0x43804380u;
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
 
+// Four pairs of fp16 numbers n - 8: nibble i of the low and of the high half of w, i = 0..3.
+__device__ __forceinline__ void centre4(uint32_t (&x)[4], uint32_t w) {
+  const uint32_t v = w >> 8;
+  x[0] = hadd2((w & 0x000f000fu) | 0x64006400u, 0xe408e408u);  // (1024 + n) - 1032
+  x[1] = hadd2((w & 0x00f000f0u) | 0x54005400u, 0xd480d480u);  // (64 + n) - 72
+  x[2] = hadd2((v & 0x000f000fu) | 0x64006400u, 0xe408e408u);
+  x[3] = hadd2((v & 0x00f000f0u) | 0x54005400u, 0xd480d480u);
+}
+// A pair of fp16 numbers n - 128: the bytes of w that kSel names (its nibbles 0 and 2).
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t centre8(uint32_t w) {
+  return hadd2(__byte_perm(w, 0x64646464u, kSel | 0x4040u), 0xe480e480u);  // (1024 + n) - 1152
+}
+
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+}
 template <int kBytes>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {  // 0 where not valid
   const int n = valid ? kBytes : 0;
@@ -150,7 +175,7 @@ __device__ __forceinline__ int kvq_swizzle(int r) {
 }
 __device__ __forceinline__ int kvq_key(int g) { return ((g >> 1) & 1) | (((g ^ (g >> 2)) & 1) << 1) | (g & 4); }
 
-template <int kBits, int kGroup, bool kDup>
+template <int kBits, int kGroup>
 struct KvqShape {
   static constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
   static constexpr int kCodeBytes = kKvqTile * kRowBytes, kParamBytes = kKvqTile * kGroups * 4;
@@ -158,8 +183,7 @@ struct KvqShape {
   // Tiles per warp in the ring: one in use, the others in flight (4 bits: 2-2.5 KB a tile, 8 bits: 4-4.5 KB).
   static constexpr int kStages = kBits == 4 ? 3 : 2;
   static constexpr int kRing = kKvqWarps * kStages * kStageBytes;
-  static constexpr int kCols = kDup ? 4 : 8;  // query rows per warp
-  static constexpr int kMerge = kKvqWarps * kCols * (128 + 2) * 4;
+  static constexpr int kMerge = kKvqWarps * 8 * (128 + 2) * 4;  // 8 rows a warp
   static constexpr int kSmem = kRing + kMerge;
 };
 
@@ -194,17 +218,16 @@ __device__ __forceinline__ void kvq_next_unit(const KvqDecodeParams& p, KvqCurso
 
 // ------------------------------------------------------------------------------------------------ split kernel
 
-// kDup: up to 4 query rows per key/value head, in columns 0-3 and again in 4-7; otherwise warps take up to 8 rows
-// each (n_rt = ceil(R / 8) row tiles) and kKvqWarps / n_rt share the keys.
-template <int kBits, int kGroup, bool kDup>
+// Warps take up to 8 query rows each: n_rt = ceil(R / 8) row tiles, and kKvqWarps / n_rt warps share the keys.
+template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const KvqDecodeParams p) {
-  using Shape = KvqShape<kBits, kGroup, kDup>;
-  constexpr int kGroups = Shape::kGroups, kRowBytes = Shape::kRowBytes, kStages = Shape::kStages, kCols = Shape::kCols;
-  constexpr int kWords = kGroup * kBits / 128;       // 32-bit words of a key row and group that a lane scores
-  constexpr int kVWords = kGroup * kBits / 256;      // words of a value row and group that a lane multiplies (or 0: half)
-  constexpr float kOffset = kBits == 4 ? 16.f : 272.f;
-  constexpr float kNone = -3e38f;                    // running max before the first key
-  extern __shared__ __align__(16) uint8_t kvq_smem[];
+  using Shape = KvqShape<kBits, kGroup>;
+  constexpr int kGroups = Shape::kGroups, kRowBytes = Shape::kRowBytes, kStages = Shape::kStages;
+  constexpr int kWords = kGroup * kBits / 128;   // 32-bit words of a key row and group that a lane scores
+  constexpr int kVWords = kGroup * kBits / 256;  // words of a value row and group that a lane multiplies (0: half a word)
+  constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
+  constexpr float kNone = -3e38f;                // running max before the first key
+  extern __shared__ __align__(128) uint8_t kvq_smem[];
   __shared__ int sh_scan[kKvqWarps];
   __shared__ int sh_b, sh_off;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
@@ -230,7 +253,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
     total += sh_scan[w];
   }
   total *= p.Hkv;
-  const int n_rt = kDup ? 1 : (R + 7) / 8;
+  const int n_rt = (R + 7) / 8;
   const int slices = kKvqWarps / n_rt;                  // warps that share the keys
   const int share = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), slices);
   const long long first64 = static_cast<long long>(blockIdx.x) * share;
@@ -264,139 +287,180 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   cur.s = kvq_seq(p, cur.b);
   cur.hk = sh_off / cur.s.tiles;
   cur.tile = sh_off % cur.s.tiles;
-  const int rt = kDup ? 0 : warp % n_rt, slice = kDup ? warp : warp / n_rt;
+  const int rt = warp % n_rt, slice = warp / n_rt;
   const bool active = slice < slices;  // (three row tiles leave two warps over)
 
-  // --- the ring
+  // --- the ring: this warp's tiles are slice, slice + slices, ... of the CTA's
   const uint32_t ring = sm100::smem_u32(kvq_smem) + warp * kStages * Shape::kStageBytes;
-  KvqCursor pre = cur;  // the next tile this warp fetches
-  pre.tile += slice;
-  int pre_lin = first + slice;
-  auto settle = [&]() {
-    while (pre.tile >= pre.s.tiles) {
-      pre.tile -= pre.s.tiles;
-      kvq_next_unit(p, pre);
-    }
-  };
+  constexpr int kChunks = kRowBytes / 16, kRowsAtOnce = 32 / kChunks;  // 16-byte chunks of a row; rows a copy covers
+  const int c_row = lane / kChunks, p_row = lane % 16;
+  // (a copy's rows are a multiple of 4 apart, and of 8 where the swizzle looks at bit 2)
+  uint32_t code_at[kKvqTile / kRowsAtOnce];
+#pragma unroll
+  for (int i = 0; i < kKvqTile / kRowsAtOnce; ++i) {
+    const int r = c_row + i * kRowsAtOnce;
+    code_at[i] = r * kRowBytes + (((lane % kChunks) ^ kvq_swizzle<kBits>(r)) << 4);
+  }
   const size_t n_rows = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_rows;
+  KvqCursor pre = cur;  // the next tile this warp fetches
+  pre.tile += slice;
+  int pre_lin = active ? first + slice : last;
+  // its first row's codes at this lane's chunk, and its params (the lower half warp fetches the keys', the upper the
+  // values')
+  const uint8_t *k_from, *v_from, *p_from;
+  size_t pre_row;
+  auto aim = [&]() {
+    pre_row = (static_cast<size_t>(pre.b) * p.Hkv + pre.hk) * p.Tk + (pre.s.start + pre.tile * kKvqTile);
+    k_from = p.k_codes + pre_row * kRowBytes + lane * 16;
+    v_from = p.v_codes + pre_row * kRowBytes + lane * 16;
+    p_from = reinterpret_cast<const uint8_t*>(lane < 16 ? p.k_params : p.v_params) +
+             (pre_row + p_row) * (kGroups * 4);
+  };
   auto fetch = [&](int stage) {  // copies (or nothing) and one commit
-    if (active && pre_lin < last) {
-      settle();
-      const int key0 = pre.s.start + pre.tile * kKvqTile, n = pre.s.L - key0;  // valid rows: n >= 1
-      const size_t row0 = (static_cast<size_t>(pre.b) * p.Hkv + pre.hk) * p.Tk + key0;
-      const uint32_t to = ring + stage * Shape::kStageBytes;
-      constexpr int kChunks = kRowBytes / 16;  // per row
-#pragma unroll
-      for (int i = 0; i < kKvqTile * kChunks / 32; ++i) {
-        const int r = lane / kChunks + i * (32 / kChunks), c = lane % kChunks;
-        const bool in = r < n && ATTN_IN_RANGE(row0 + r, 1, n_rows, kSiteKvqDecCodes, &g_kvq_error);
-        const size_t from = in ? (row0 + r) * kRowBytes + c * 16 : 0;
-        const uint32_t at = to + r * kRowBytes + ((c ^ kvq_swizzle<kBits>(r)) << 4);
-        cp_async<16>(at, p.k_codes + from, in);
-        cp_async<16>(at + Shape::kCodeBytes, p.v_codes + from, in);
+    if (pre_lin < last) {
+      if (pre.tile >= pre.s.tiles) {
+        do {
+          pre.tile -= pre.s.tiles;
+          kvq_next_unit(p, pre);
+        } while (pre.tile >= pre.s.tiles);
+        aim();
       }
-      const int r = lane % 16;
-      const bool in = r < n && ATTN_IN_RANGE(row0 + r, 1, n_rows, kSiteKvqDecParams, &g_kvq_error);
-      cp_async<kGroups * 4>(to + 2 * Shape::kCodeBytes + lane * kGroups * 4,
-                            (lane < 16 ? p.k_params : p.v_params) + (in ? (row0 + r) * kGroups : 0), in);
+      const int n = pre.s.L - (pre.s.start + pre.tile * kKvqTile);  // valid rows (at least one)
+      const uint32_t to = ring + stage * Shape::kStageBytes;
+      const uint32_t p_to = to + 2 * Shape::kCodeBytes + lane * kGroups * 4;
+      if (n >= kKvqTile && ATTN_IN_RANGE(pre_row, kKvqTile, n_rows, kSiteKvqDecCodes, &g_kvq_error)) {
+#pragma unroll
+        for (int i = 0; i < kKvqTile / kRowsAtOnce; ++i) {
+          cp_async<16>(to + code_at[i], k_from + i * 512);
+          cp_async<16>(to + code_at[i] + Shape::kCodeBytes, v_from + i * 512);
+        }
+        cp_async<kGroups * 4>(p_to, p_from);
+      } else {  // rows past the sequence's end are zeros, and not read
+#pragma unroll
+        for (int i = 0; i < kKvqTile / kRowsAtOnce; ++i) {
+          const int r = c_row + i * kRowsAtOnce;
+          const bool in = r < n && ATTN_IN_RANGE(pre_row + r, 1, n_rows, kSiteKvqDecCodes, &g_kvq_error);
+          cp_async<16>(to + code_at[i], in ? k_from + i * 512 : p.k_codes, in);
+          cp_async<16>(to + code_at[i] + Shape::kCodeBytes, in ? v_from + i * 512 : p.v_codes, in);
+        }
+        const bool in = p_row < n && ATTN_IN_RANGE(pre_row + p_row, 1, n_rows, kSiteKvqDecParams, &g_kvq_error);
+        cp_async<kGroups * 4>(p_to, in ? p_from : reinterpret_cast<const uint8_t*>(p.k_params), in);
+      }
+      const uint32_t rows = slices * kKvqTile;
       pre_lin += slices;
       pre.tile += slices;
+      pre_row += rows;
+      k_from += rows * kRowBytes;
+      v_from += rows * kRowBytes;
+      p_from += rows * (kGroups * 4);
     }
     cp_async_commit();
   };
+  if (pre.tile < pre.s.tiles) aim();
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
+  // Where this lane reads a tile. Keys: row kg (and kg + 8), its words of each group. Values: rows vk0, vk1 (and + 8),
+  // which are the columns 2 t, 2 t + 1 (and + 8) of the value fragments.
+  const int kg = kvq_key(g), vk0 = kvq_key(2 * t), vk1 = kvq_key(2 * t + 1);
+  const int v_byte = kVWords < 1 ? (g >> 1) * 4 : g * kVWords * 4;
+  auto at_byte = [](int row, int byte) {
+    return row * kRowBytes + (((byte >> 4) ^ kvq_swizzle<kBits>(row)) << 4) + (byte & 15);
+  };
+  const uint32_t k_lds = at_byte(kg, t * kWords * 4), kp_lds = 2 * Shape::kCodeBytes + kg * kGroups * 4;
+  const uint32_t v0_lds = Shape::kCodeBytes + at_byte(vk0, v_byte), v1_lds = Shape::kCodeBytes + at_byte(vk1, v_byte);
+
   float* mg_o = reinterpret_cast<float*>(kvq_smem + Shape::kRing);        // [warp][column][128]
-  float* mg_ml = mg_o + kKvqWarps * kCols * 128;                         // [warp][column][2]
+  float* mg_ml = mg_o + kKvqWarps * 8 * 128;                             // [warp][column][2]
   const size_t n_q = static_cast<size_t>(p.B) * p.Tq * p.H * 128;
   (void)n_q;
 
   int stage = 0, lin = first;  // lin: first tile of the current piece
-  int mine = first + slice;    // this warp's next tile
+  int mine = active ? first + slice : last;  // this warp's next tile
   while (lin < last) {
     // --- one piece: tiles [lin, piece_end) of unit (cur.b, cur.hk), from its tile cur.tile on
     const int piece_end = min(last, lin + cur.s.tiles - cur.tile);
     const bool whole = cur.tile == 0 && piece_end - lin == cur.s.tiles;
-    // The unit's queries as B fragments: column g is row `row`; the lane holds its dims that meet word w of group j
-    // of a key row, paired as the codes' nibbles are.
-    const int row = kDup ? (g & 3) : rt * 8 + g;
+    // The unit's queries as B fragments: column g is row rt * 8 + g; the lane holds its dims that meet the words of a
+    // key row that it reads, paired as the codes are, in units of 2^-up.
     uint32_t qb[16];
     float qsum[kGroups][2];  // per group, the sum of q over its dims, of columns 2 t and 2 t + 1
+    float down[2];           // softmax scale (log2 units) times 2^-up of columns 2 t and 2 t + 1
     {
-      const int i = row % p.Tq, h = cur.hk * G + row / p.Tq;
+      const int row = rt * 8 + g, i = row % p.Tq, h = cur.hk * G + row / p.Tq;
       const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128;
       const bool live = row < R && ATTN_IN_RANGE(off, 128, n_q, kSiteKvqDecQ, &g_kvq_error);
+      uint4 u[4];
+      uint32_t top = 0;  // the largest exponent, bf16 bits 7-14 of a half
 #pragma unroll
-      for (int j = 0; j < kGroups; ++j) {
-        float part = 0.f;
-#pragma unroll
-        for (int e = 0; e < kGroup / 32; ++e) {  // 8 dims at a time
-          const int x = j * (kGroup / 32) + e;
-          uint4 u = make_uint4(0u, 0u, 0u, 0u);
-          if (live) u = *reinterpret_cast<const uint4*>(p.q + off + j * kGroup + t * (kGroup / 4) + 8 * e);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) part += __uint_as_float(w[y] << 16) + __uint_as_float(w[y] & 0xffff0000u);
-          if constexpr (kBits == 4) {  // dims (0,4) (1,5) (2,6) (3,7) of a word's eight
-            qb[4 * x] = __byte_perm(w[0], w[2], 0x5410);
-            qb[4 * x + 1] = __byte_perm(w[0], w[2], 0x7632);
-            qb[4 * x + 2] = __byte_perm(w[1], w[3], 0x5410);
-            qb[4 * x + 3] = __byte_perm(w[1], w[3], 0x7632);
-          } else {  // dims (0,2) (1,3) of each word's four
-            qb[4 * x] = __byte_perm(w[0], w[1], 0x5410);
-            qb[4 * x + 1] = __byte_perm(w[0], w[1], 0x7632);
-            qb[4 * x + 2] = __byte_perm(w[2], w[3], 0x5410);
-            qb[4 * x + 3] = __byte_perm(w[2], w[3], 0x7632);
-          }
-        }
-        part += __shfl_xor_sync(0xffffffffu, part, 1);
-        part += __shfl_xor_sync(0xffffffffu, part, 2);
-        qsum[j][0] = __shfl_sync(0xffffffffu, part, 8 * t);
-        qsum[j][1] = __shfl_sync(0xffffffffu, part, 8 * t + 4);
+      for (int x = 0; x < 4; ++x) {
+        u[x] = make_uint4(0u, 0u, 0u, 0u);
+        const int j = x / (kGroup / 32), e = x % (kGroup / 32);  // 8 dims of group j
+        if (live) u[x] = *reinterpret_cast<const uint4*>(p.q + off + j * kGroup + t * (kGroup / 4) + 8 * e);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(u[x].x & 0x7f807f80u, u[x].y & 0x7f807f80u),
+                                     __vmaxu2(u[x].z & 0x7f807f80u, u[x].w & 0x7f807f80u)));
       }
-    }
-    // Keys that columns 2 t and 2 t + 1 see: [see_lo, see_hi].
-    int see_lo[2], see_hi[2];
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^up brings exponent `top` to 2^10 (an infinity or NaN stays one); 2^up and 2^-up are normal numbers
+      const int up = min(10 + 127 - static_cast<int>(top >> 7), 126);
+      const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+      float part = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = 2 * t + c, r = kDup ? (col & 3) : rt * 8 + col;
-      see_hi[c] = cur.s.L - p.Tq + r % p.Tq;
-      see_lo[c] = p.window < 0 ? 0 : see_hi[c] - p.window;
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t w[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float a = __uint_as_float(w[y] << 16) * mul, b = __uint_as_float(w[y] & 0xffff0000u) * mul;
+          f[y] = pack_f16x2(a, b);
+          part += a + b;
+        }
+        if constexpr (kBits == 4) {  // dims (0,4) (1,5) (2,6) (3,7) of a word's eight
+          qb[4 * x] = __byte_perm(f[0], f[2], 0x5410);
+          qb[4 * x + 1] = __byte_perm(f[0], f[2], 0x7632);
+          qb[4 * x + 2] = __byte_perm(f[1], f[3], 0x5410);
+          qb[4 * x + 3] = __byte_perm(f[1], f[3], 0x7632);
+        } else {  // dims (0,1) (2,3) of each word's four
+#pragma unroll
+          for (int y = 0; y < 4; ++y) qb[4 * x + y] = f[y];
+        }
+        if ((x + 1) % (kGroup / 32) == 0) {
+          const int j = x / (kGroup / 32);
+          part += __shfl_xor_sync(0xffffffffu, part, 1);
+          part += __shfl_xor_sync(0xffffffffu, part, 2);
+          qsum[j][0] = __shfl_sync(0xffffffffu, part, 8 * t);
+          qsum[j][1] = __shfl_sync(0xffffffffu, part, 8 * t + 4);
+          part = 0.f;
+        }
+      }
+      const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+      down[0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      down[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
     float acc[8][4], corr[kGroups][2], m[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
+    float unit[kGroups], most[kGroups];  // value weights are in units of 1 / unit; most: the largest scale that fits
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = 0.f;
+    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = most[j] = 0.f, unit[j] = 1.f;
 
-    for (; active && mine < piece_end; mine += slices) {
-      const int key0 = cur.s.start + (cur.tile + mine - lin) * kKvqTile;
-      cp_async_wait<kStages - 2>();
-      __syncwarp();  // this tile is in, and every lane has read the one before it
-      fetch(stage == 0 ? kStages - 1 : stage - 1);
-      const uint32_t at = ring + stage * Shape::kStageBytes;
-      const uint32_t kp_at = at + 2 * Shape::kCodeBytes, vp_at = kp_at + Shape::kParamBytes;
-      const int kg = kvq_key(g);
+    auto tile = [&](const uint32_t at, const int key0, auto masked) {
       // --- scores: rows g and g + 8 are keys kg and kg + 8
       float s[4] = {0.f, 0.f, 0.f, 0.f};
       {
         uint32_t sz[2][kGroups];
-        lds(sz[0], kp_at + kg * kGroups * 4);
-        lds(sz[1], kp_at + (kg + 8) * kGroups * 4);
-        const uint32_t row_at = at + kg * kRowBytes;
-        const int sw = kvq_swizzle<kBits>(kg);  // (the same for kg + 8)
+        lds(sz[0], at + kp_lds);
+        lds(sz[1], at + kp_lds + 8 * kGroups * 4);
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
-          float c[4];
-          c[0] = c[2] = -kOffset * qsum[j][0];
-          c[1] = c[3] = -kOffset * qsum[j][1];
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
           constexpr int kPart = kWords < 4 ? kWords : 4;  // words read at once
 #pragma unroll
           for (int w0 = 0; w0 < kWords; w0 += kPart) {
-            const int byte = j * (kGroup * kBits / 8) + t * kWords * 4 + w0 * 4;
-            const uint32_t a = row_at + (((byte >> 4) ^ sw) << 4) + (byte & 15);
+            const uint32_t a = (at + k_lds) ^ (j * (kGroup * kBits / 8) + w0 * 4);
             uint32_t ka[kPart], kb[kPart];
             lds(ka, a);
             lds(kb, a + 8 * kRowBytes);
@@ -404,133 +468,151 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
             for (int w = 0; w < kPart; ++w) {
               if constexpr (kBits == 4) {
                 const uint32_t* b = qb + 4 * (j * kWords + w0 + w);
-                mma_16x8x16(c, nibbles<0, kMagic16>(ka[w]), nibbles<0, kMagic16>(kb[w]), nibbles<1, kMagic16>(ka[w]),
-                            nibbles<1, kMagic16>(kb[w]), b[0], b[1]);
-                mma_16x8x16(c, nibbles<2, kMagic16>(ka[w]), nibbles<2, kMagic16>(kb[w]), nibbles<3, kMagic16>(ka[w]),
-                            nibbles<3, kMagic16>(kb[w]), b[2], b[3]);
+                uint32_t xa[4], xb[4];
+                centre4(xa, ka[w]);
+                centre4(xb, kb[w]);
+                mma_16x8x16(c, xa[0], xb[0], xa[1], xb[1], b[0], b[1]);
+                mma_16x8x16(c, xa[2], xb[2], xa[3], xb[3], b[2], b[3]);
               } else {
                 const uint32_t* b = qb + 2 * (j * kWords + w0 + w);
-                mma_16x8x16(c, nibbles<0, kMagic16>(ka[w]), nibbles<0, kMagic16>(kb[w]), nibbles<2, kMagic16>(ka[w]),
-                            nibbles<2, kMagic16>(kb[w]), b[0], b[1]);
-                mma_16x8x16(c, nibbles<1, kMagic256>(ka[w]), nibbles<1, kMagic256>(kb[w]), nibbles<3, kMagic256>(ka[w]),
-                            nibbles<3, kMagic256>(kb[w]), b[0], b[1]);
+                mma_16x8x16(c, centre8<0x0100>(ka[w]), centre8<0x0100>(kb[w]), centre8<0x0302>(ka[w]),
+                            centre8<0x0302>(kb[w]), b[0], b[1]);
               }
             }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[e] = fmaf(__uint_as_float(sz[e / 2][j] << 16), c[e],
-                        fmaf(__uint_as_float(sz[e / 2][j] & 0xffff0000u), qsum[j][e & 1], s[e]));
+          for (int y = 0; y < 2; ++y) {
+            const float sc = __uint_as_float(sz[y][j] << 16);
+            const float zc = fmaf(kCentre, sc, __uint_as_float(sz[y][j] & 0xffff0000u));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[2 * y + e] = fmaf(sc, c[2 * y + e], fmaf(zc, qsum[j][e], s[2 * y + e]));
+          }
         }
       }
       // --- softmax: keys past a row's last (or before its window) have weight 0, whatever they hold
-      const bool all_seen = key0 + kKvqTile - 1 <= cur.s.L - p.Tq && (p.window < 0 || key0 >= cur.s.L - 1 - p.window);
+      uint32_t vsz[2][kGroups];
+      lds(vsz[0], at + kp_lds + Shape::kParamBytes);
+      lds(vsz[1], at + kp_lds + Shape::kParamBytes + 8 * kGroups * 4);
       bool seen[4] = {true, true, true, true};
-      if (!all_seen) {
+      if constexpr (masked.value) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int key = key0 + kg + 8 * (e / 2);
-          seen[e] = key >= see_lo[e & 1] && key <= see_hi[e & 1];
+          const int key = key0 + kg + 8 * (e / 2), hi = cur.s.L - p.Tq + (rt * 8 + 2 * t + (e & 1)) % p.Tq;
+          seen[e] = key <= hi && (p.window < 0 || key >= hi - p.window);
         }
       }
+      float x[4];  // log2 of the weights
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = seen[e] ? s[e] * p.scale_log2 : -INFINITY;
-      const bool raise = s[0] > m[0] + 8.f || s[2] > m[0] + 8.f || s[1] > m[1] + 8.f || s[3] > m[1] + 8.f;
+      for (int e = 0; e < 4; ++e) x[e] = seen[e] ? fmaf(s[e], down[e & 1], -m[e & 1]) : -INFINITY;
+      bool raise = x[0] > 8.f || x[1] > 8.f || x[2] > 8.f || x[3] > 8.f;
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j)
+        raise = raise || __uint_as_float(vsz[0][j] << 16) > most[j] || __uint_as_float(vsz[1][j] << 16) > most[j];
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float x = fmaxf(fmaxf(s[c], s[c + 2]), m[c]);
+          float y = m[c];  // the new max
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-          const float f = ex2(m[c] - x);
-          m[c] = x;
+          for (int e = c; e < 4; e += 2)
+            if (seen[e]) y = fmaxf(y, s[e] * down[c]);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+          const float f = ex2(m[c] - y);
+          m[c] = y;
+#pragma unroll
+          for (int e = c; e < 4; e += 2)
+            if (seen[e]) x[e] = fmaf(s[e], down[c], -y);
           l[c] *= f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[i][c] *= f, acc[i][c + 2] *= f;
 #pragma unroll
           for (int j = 0; j < kGroups; ++j) corr[j][c] *= f;
         }
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+          float y = fmaxf(__uint_as_float(vsz[0][j] << 16), __uint_as_float(vsz[1][j] << 16));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+          if (y > most[j]) {
+            const int e = max(static_cast<int>(__float_as_uint(y) >> 23), 1);  // exponent field of the largest scale
+            const float to = __uint_as_float(static_cast<uint32_t>(max(254 - e, 1)) << 23);  // 2^-(e - 127)
+            const float f = most[j] == 0.f ? 0.f : to / unit[j];  // (no sums yet: they are 0)
+            unit[j] = to;
+            most[j] = __uint_as_float(static_cast<uint32_t>(min(e + 5, 254)) << 23);
+#pragma unroll
+            for (int i = j * (kGroup / 16); i < (j + 1) * (kGroup / 16); ++i)
+              acc[i][0] *= f, acc[i][1] *= f, acc[i][2] *= f, acc[i][3] *= f;
+          }
+        }
       }
       float pr[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pr[e] = ex2(s[e] - m[e & 1]);
+      for (int e = 0; e < 4; ++e) pr[e] = ex2(x[e]);
       l[0] += pr[0] + pr[2];
       l[1] += pr[1] + pr[3];
       // --- values
-      {
-        uint32_t sz[2][kGroups];
-        lds(sz[0], vp_at + kg * kGroups * 4);
-        lds(sz[1], vp_at + (kg + 8) * kGroups * 4);
-        // the lane's four keys of a value tile: A fragment columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-        const int k0 = kvq_key(2 * t), k1 = kvq_key(2 * t + 1);
-        const uint32_t v_at = at + Shape::kCodeBytes;
-        const int sw0 = kvq_swizzle<kBits>(k0), sw1 = kvq_swizzle<kBits>(k1);
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-          uint32_t hi[2], lo[2];  // p s of keys kg (+ 8) and columns 2 t, 2 t + 1, in two bf16 parts
+      for (int j = 0; j < kGroups; ++j) {
+        uint32_t b[2];  // the weights of keys kg (+ 8) and columns 2 t, 2 t + 1, then transposed
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float sc = __uint_as_float(sz[y][j] << 16), z = __uint_as_float(sz[y][j] & 0xffff0000u);
-            const float zo = fmaf(-kOffset, sc, z);
-            float v0 = pr[2 * y] * sc, v1 = pr[2 * y + 1] * sc;
-            float d0 = pr[2 * y] * zo, d1 = pr[2 * y + 1] * zo;
-            if (!all_seen) {  // (a NaN in a key that a row does not see stays out of it)
-              v0 = seen[2 * y] ? v0 : 0.f, v1 = seen[2 * y + 1] ? v1 : 0.f;
-              d0 = seen[2 * y] ? d0 : 0.f, d1 = seen[2 * y + 1] ? d1 : 0.f;
-            }
-            corr[j][0] += d0;
-            corr[j][1] += d1;
-            const uint32_t h = sm100::pack_bf16x2(v0, v1);
-            const uint32_t e = sm100::pack_bf16x2(v0 - __uint_as_float(h << 16), v1 - __uint_as_float(h & 0xffff0000u));
-            if constexpr (kDup) {
-              hi[y] = movmatrix(t < 2 ? h : e);
-            } else {
-              hi[y] = movmatrix(h);
-              lo[y] = movmatrix(e);
-            }
+        for (int y = 0; y < 2; ++y) {
+          const float sc = __uint_as_float(vsz[y][j] << 16);
+          const float zc = fmaf(kCentre, sc, __uint_as_float(vsz[y][j] & 0xffff0000u));
+          const float su = sc * unit[j];
+          float w0 = pr[2 * y] * su, w1 = pr[2 * y + 1] * su;
+          if constexpr (masked.value) {  // (a NaN in a key that a row does not see stays out of it)
+            if (!seen[2 * y]) w0 = 0.f;
+            if (!seen[2 * y + 1]) w1 = 0.f;
+            if (seen[2 * y]) corr[j][0] = fmaf(pr[2 * y], zc, corr[j][0]);
+            if (seen[2 * y + 1]) corr[j][1] = fmaf(pr[2 * y + 1], zc, corr[j][1]);
+          } else {
+            corr[j][0] = fmaf(pr[2 * y], zc, corr[j][0]);
+            corr[j][1] = fmaf(pr[2 * y + 1], zc, corr[j][1]);
           }
-          auto mul = [&](float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-            mma_16x8x16(c, a0, a1, a2, a3, hi[0], hi[1]);
-            if constexpr (!kDup) mma_16x8x16(c, a0, a1, a2, a3, lo[0], lo[1]);
-          };
-          // Words w of the lane's dims j * kGroup + g * (kGroup / 8) + ...: eight (4 bits) or four (8 bits) dims of
-          // each key; with 4 bits and groups of 32 the lane's four dims are half a word.
-          constexpr int kRead = kVWords < 1 ? 1 : kVWords;
-          const int byte = j * (kGroup * kBits / 8) + (kVWords < 1 ? (g >> 1) * 4 : g * kVWords * 4);
-          uint32_t va[kRead], vb[kRead], vc[kRead], vd[kRead];
-          const uint32_t a0 = v_at + k0 * kRowBytes + (((byte >> 4) ^ sw0) << 4) + (byte & 15);
-          const uint32_t a1 = v_at + k1 * kRowBytes + (((byte >> 4) ^ sw1) << 4) + (byte & 15);
-          lds(va, a0);
-          lds(vb, a1);
-          lds(vc, a0 + 8 * kRowBytes);
-          lds(vd, a1 + 8 * kRowBytes);
-          constexpr int kTiles = kGroup / 16;  // tiles of 16 dims in the group
-          if constexpr (kBits == 4) {
+          b[y] = movmatrix(pack_f16x2(w0, w1));
+        }
+        // The lane's dims j * kGroup + g * (kGroup / 8) + ... of its four keys: eight dims a word (4 bits) or four (8
+        // bits); with 4 bits and groups of 32 the lane's four dims are half a word.
+        constexpr int kRead = kVWords < 1 ? 1 : kVWords;
+        const uint32_t a0 = (at + v0_lds) ^ (j * (kGroup * kBits / 8)), a1 = (at + v1_lds) ^ (j * (kGroup * kBits / 8));
+        uint32_t va[kRead], vb[kRead], vc[kRead], vd[kRead];
+        lds(va, a0);
+        lds(vb, a1);
+        lds(vc, a0 + 8 * kRowBytes);
+        lds(vd, a1 + 8 * kRowBytes);
+        constexpr int kTiles = kGroup / 16;  // tiles of 16 dims in the group
 #pragma unroll
-            for (int r = 0; r < kGroup / 32; ++r) {  // four dims at a time: half a word of each key
-              const uint32_t sel = kVWords < 1 ? ((g & 1) ? 0x7632u : 0x5410u) : ((r & 1) ? 0x7632u : 0x5410u);
-              const uint32_t x = __byte_perm(va[r / 2], vb[r / 2], sel), y = __byte_perm(vc[r / 2], vd[r / 2], sel);
-              mul(acc[j * kTiles + 2 * r], nibbles<0, kMagic16>(x), nibbles<1, kMagic16>(x), nibbles<0, kMagic16>(y),
-                  nibbles<1, kMagic16>(y));
-              mul(acc[j * kTiles + 2 * r + 1], nibbles<2, kMagic16>(x), nibbles<3, kMagic16>(x),
-                  nibbles<2, kMagic16>(y), nibbles<3, kMagic16>(y));
-            }
+        for (int r = 0; r < kGroup / 32; ++r) {  // four dims at a time
+          if constexpr (kBits == 4) {
+            const uint32_t sel = (kVWords < 1 ? g & 1 : r & 1) ? 0x7632u : 0x5410u;
+            uint32_t x[4], y[4];
+            centre4(x, __byte_perm(va[r / 2], vb[r / 2], sel));
+            centre4(y, __byte_perm(vc[r / 2], vd[r / 2], sel));
+            mma_16x8x16(acc[j * kTiles + 2 * r], x[0], x[1], y[0], y[1], b[0], b[1]);
+            mma_16x8x16(acc[j * kTiles + 2 * r + 1], x[2], x[3], y[2], y[3], b[0], b[1]);
           } else {
 #pragma unroll
-            for (int r = 0; r < kGroup / 32; ++r) {  // four dims: a word of each key
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t sel = h ? 0x7632u : 0x5410u;
-                const uint32_t x = __byte_perm(va[r], vb[r], sel), y = __byte_perm(vc[r], vd[r], sel);
-                mul(acc[j * kTiles + 2 * r + h], nibbles<0, kMagic16>(x), nibbles<2, kMagic16>(x),
-                    nibbles<0, kMagic16>(y), nibbles<2, kMagic16>(y));
-                mul(acc[j * kTiles + 2 * r + h], nibbles<1, kMagic256>(x), nibbles<3, kMagic256>(x),
-                    nibbles<1, kMagic256>(y), nibbles<3, kMagic256>(y));
-              }
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t sel = h ? 0x7632u : 0x5410u;
+              const uint32_t x = __byte_perm(va[r], vb[r], sel), y = __byte_perm(vc[r], vd[r], sel);
+              mma_16x8x16(acc[j * kTiles + 2 * r + h], centre8<0x0200>(x), centre8<0x0301>(x), centre8<0x0200>(y),
+                          centre8<0x0301>(y), b[0], b[1]);
             }
           }
         }
       }
+    };
+
+    for (; mine < piece_end; mine += slices) {
+      const int key0 = cur.s.start + (cur.tile + mine - lin) * kKvqTile;
+      cp_async_wait<kStages - 2>();
+      __syncwarp();  // this tile is in, and every lane has read the one before it
+      fetch(stage == 0 ? kStages - 1 : stage - 1);
+      const uint32_t at = ring + stage * Shape::kStageBytes;
+      if (key0 + kKvqTile - 1 <= cur.s.L - p.Tq && (p.window < 0 || key0 >= cur.s.L - 1 - p.window))
+        tile(at, key0, std::false_type());  // every row sees every key
+      else
+        tile(at, key0, std::true_type());
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
@@ -544,38 +626,32 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
         for (int j = 0; j < kGroups; ++j) corr[j][c] += __shfl_xor_sync(0xffffffffu, corr[j][c], o);
       }
     }
+    float worth[kGroups];
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) worth[j] = 1.f / unit[j];
     __syncthreads();  // the previous piece's parts have been read
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int j = i / (kGroup / 16), dim = j * kGroup + g * (kGroup / 8) + 2 * (i % (kGroup / 16));
+    for (int c = 0; c < 2; ++c) {
+      const int col = warp * 8 + 2 * t + c;
+      if (rt * 8 + 2 * t + c >= R) continue;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float x = acc[i][c], y = acc[i][c + 2];
-        if constexpr (kDup) {
-          x += __shfl_xor_sync(0xffffffffu, x, 2);
-          y += __shfl_xor_sync(0xffffffffu, y, 2);
-        }
-        if (!kDup || t < 2)
-          *reinterpret_cast<float2*>(mg_o + (warp * kCols + 2 * t + c) * 128 + dim) =
-              make_float2(x + corr[j][c], y + corr[j][c]);
+      for (int i = 0; i < 8; ++i) {
+        const int j = i / (kGroup / 16), dim = j * kGroup + g * (kGroup / 8) + 2 * (i % (kGroup / 16));
+        *reinterpret_cast<float2*>(mg_o + col * 128 + dim) =
+            make_float2(fmaf(acc[i][c], worth[j], corr[j][c]), fmaf(acc[i][c + 2], worth[j], corr[j][c]));
       }
-    }
-    if (g == 0 && (!kDup || t < 2)) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        *reinterpret_cast<float2*>(mg_ml + (warp * kCols + 2 * t + c) * 2) = make_float2(m[c], l[c]);
+      if (g == 0) *reinterpret_cast<float2*>(mg_ml + col * 2) = make_float2(m[c], l[c]);
     }
     __syncthreads();
     const int slot = lin == first ? 0 : 1;
     for (int e = tid; e < R * 32; e += kKvqThreads) {
       const int r = e / 32, d = (e % 32) * 4;
-      const int w0 = kDup ? 0 : r / 8, col = kDup ? r : r % 8, step = kDup ? 1 : n_rt;
       float M = kNone;
-      for (int s = 0; s < slices; ++s) M = fmaxf(M, mg_ml[((w0 + s * step) * kCols + col) * 2]);
+      for (int s = 0; s < slices; ++s) M = fmaxf(M, mg_ml[((r / 8 + s * n_rt) * 8 + r % 8) * 2]);
       float L = 0.f;
       float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int s = 0; s < slices; ++s) {
-        const int at = (w0 + s * step) * kCols + col;
+        const int at = (r / 8 + s * n_rt) * 8 + r % 8;
         const float f = ex2(mg_ml[at * 2] - M);
         L = fmaf(mg_ml[at * 2 + 1], f, L);
         const float4 x = *reinterpret_cast<const float4*>(mg_o + at * 128 + d);

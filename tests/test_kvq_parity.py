@@ -11,8 +11,9 @@ Tolerances, derived from the arithmetic:
             terms' sizes, scale * sum_d |q_d| (|z| + c s), where c = 2 * 2^bits covers codes that are carried with
             an offset of up to 2^bits + 16. lse is off by the largest dS of its keys, plus the fp32 rounding of
             the running max and sum (2^-20, and 2^-22 of its value).
-  o       : one bf16 rounding, 2^-8 |o|; each weight is off by 2 dS + 2^-14 of itself (exp2 and the running sums
-            in fp32, a weight carried to 16 bits), each counted against sum_j p_j (|z| + c s).
+  o       : one bf16 rounding, 2^-8 |o|; each weight is off by 2 dS + 2^-14 of itself (exp2 and the running sums in
+            fp32), counted against sum_j p_j (|z| + c s); and the product of a weight and a scale is rounded to fp16,
+            2^-11 of itself, before it multiplies a code, centred or not, of at most 2^bits: 2^-11 sum_j p_j 2^bits s.
 """
 import numpy as np
 import pytest
@@ -197,6 +198,7 @@ def check_decode(q, cache, lens, scale, window, o, lse, what):
             k, v = (dequantize(t[b, h // G, :L].numpy(), p[b, h // G, :L], bits) for t, p in ((kc, kp), (vc, vp)))
             ks, vs = (np.repeat(np.abs(cpu(p[b, h // G, :L, :, 1])) + c * cpu(p[b, h // G, :L, :, 0]), D // p.shape[3], -1)
                       for p in (kp, vp))
+            vstep = np.repeat(cpu(vp[b, h // G, :L, :, 0]), D // vp.shape[3], -1)
             for i in range(Tq):
                 last = L - Tq + i
                 w = f"{what} b={b} h={h} i={i}"
@@ -208,6 +210,7 @@ def check_decode(q, cache, lens, scale, window, o, lse, what):
                 assert abs(lse[b, h, i] - LSE[b, h, i]) <= dS + 2.0 ** -20 + 2.0 ** -22 * abs(LSE[b, h, i]), w
                 p = np.exp(scale * (k[first:last + 1] @ q64[b, i, h]) - LSE[b, h, i])
                 tol = 2.0 ** -8 * np.abs(O[b, i, h]) + (2 * dS + 2.0 ** -14) * (p @ vs[first:last + 1])
+                tol += 2.0 ** -11 * 2 ** bits * (p @ vstep[first:last + 1])
                 err = np.abs(o[b, i, h] - O[b, i, h])
                 assert (err <= tol).all(), f"{w}: {(err / tol).max():.2f} of the tolerance"
 
