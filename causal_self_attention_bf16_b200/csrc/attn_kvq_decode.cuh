@@ -9,19 +9,19 @@
 // read, to fill 128-row tiles with 1 to 32 queries. What bounds the loop is the widening itself, so it is kept to
 // few operations, spread over the integer and the floating-point pipe:
 //
-//   Codes. In fp16, 0x6400 | n is 1024 + n for n up to 1023 and 0x5400 | n << 4 is 64 + n for n up to 15, exactly. So
-//   two of the four nibbles of a 16-bit half need no shift at all and the other two share one, and one logical
-//   operation makes a pair of them numbers; 8-bit codes take one byte permutation a pair. One packed addition then
-//   centres them, n - 8 or n - 128, exactly: small sums of both signs, which cost the fp32 accumulators little.
-//   Scores. For key j and query row r, with c the centre and the sums taken group by group of dims:
-//     q . k = sum_g s_g (sum_d q_d (n_d - c)) + (z_g + c s_g) (sum_d q_d).   The first sum is the matrix product, the
-//   last is made once per query row. A query row is scaled by a power of two that puts its largest dim into
-//   [2^10, 2^11), so that its bf16 numbers are fp16 numbers (exactly down to 2^-24, 2^-34 of the largest), and the
-//   power is taken off with the softmax scale.
-//   Values. o = sum_j p_j s_g (n - c) + sum_j p_j (z_g + c s_g). p_j s_g is the B fragment, rounded to fp16: 2^-11 of
-//   itself at most against the output's own 2^-8. So that it is in fp16's range whatever the scales, it is carried in
-//   units of a power of two per group of dims, raised when a key's scale passes it by 2^5 (and the sums rescaled). The
-//   second sum is fp32 throughout.
+//   Codes. A small integer in the low bits of an fp16 number is that number: n * 2^-24, a subnormal, which the matrix
+//   unit multiplies exactly. So one logical operation makes two numbers of a 32-bit word's low nibbles (n * 2^-24), of
+//   its second nibbles (n * 2^-20, without a shift), and after one shift of the third and fourth; 8-bit codes take a
+//   byte permutation a pair. The powers of two go into the queries' numbers and, for values, into the result's.
+//   Scores. For key j and query row r, with the sums taken group by group of dims:
+//     q . k = sum_g s_g (sum_d q_d n_d) + z_g (sum_d q_d).     The first sum is the matrix product, the last is made
+//   once per query row. A query row is scaled by a power of two that puts its largest dim into [2^14, 2^15), so that
+//   its bf16 numbers are fp16 numbers (exactly down to 2^-34 of the largest); the power goes off with the softmax scale.
+//   Values. o = sum_j p_j s_g (n - c) + sum_j p_j (z_g + c s_g), c = 8 or 128: one packed addition centres the codes, so
+//   that the fp32 accumulators hold sums of both signs, whose roundings stay small however long the cache. p_j s_g is
+//   the B fragment, rounded to fp16: 2^-11 of itself at most against the output's own 2^-8. So that it is in fp16's
+//   range whatever the scales, it is carried in units of a power of two per group of dims, raised when a key's scale
+//   passes it by 2^5 (and the sums rescaled). The second sum is fp32 throughout.
 //   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 8 (then p <= 2^8
 //   and the sums stay far from overflow): one vote a tile in place of the reduction and the rescaling.
 //
@@ -91,6 +91,14 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with c = 0 before.
+__device__ __forceinline__ void mma_16x8x16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                  uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Transpose of an 8 x 8 matrix of 16-bit numbers held two to a lane.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
@@ -114,18 +122,25 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   return c;
 }
 
-// Four pairs of fp16 numbers n - 8: nibble i of the low and of the high half of w, i = 0..3.
-__device__ __forceinline__ void centre4(uint32_t (&x)[4], uint32_t w) {
+// Nibbles 0..3 of the low and of the high half of w as fp16 numbers n * 2^-24 (x[0], x[2]) and n * 2^-20 (x[1], x[3]);
+// centred: n - 8.
+template <bool kCentred>
+__device__ __forceinline__ void widen4(uint32_t (&x)[4], uint32_t w) {
   const uint32_t v = w >> 8;
-  x[0] = hadd2((w & 0x000f000fu) | 0x64006400u, 0xe408e408u);  // (1024 + n) - 1032
-  x[1] = hadd2((w & 0x00f000f0u) | 0x54005400u, 0xd480d480u);  // (64 + n) - 72
-  x[2] = hadd2((v & 0x000f000fu) | 0x64006400u, 0xe408e408u);
-  x[3] = hadd2((v & 0x00f000f0u) | 0x54005400u, 0xd480d480u);
+  x[0] = w & 0x000f000fu;
+  x[1] = w & 0x00f000f0u;
+  x[2] = v & 0x000f000fu;
+  x[3] = v & 0x00f000f0u;
+  if constexpr (kCentred) {
+    x[0] = hadd2(x[0], 0x80088008u), x[1] = hadd2(x[1], 0x80808080u);
+    x[2] = hadd2(x[2], 0x80088008u), x[3] = hadd2(x[3], 0x80808080u);
+  }
 }
-// A pair of fp16 numbers n - 128: the bytes of w that kSel names (its nibbles 0 and 2).
-template <uint32_t kSel>
-__device__ __forceinline__ uint32_t centre8(uint32_t w) {
-  return hadd2(__byte_perm(w, 0x64646464u, kSel | 0x4040u), 0xe480e480u);  // (1024 + n) - 1152
+// The bytes of w that kSel names (its nibbles 0 and 2) as fp16 numbers n * 2^-24; centred: n - 128.
+template <bool kCentred, uint32_t kSel>
+__device__ __forceinline__ uint32_t widen8(uint32_t w) {
+  const uint32_t x = __byte_perm(w, 0u, kSel | 0x4040u);
+  return kCentred ? hadd2(x, 0x80808080u) : x;
 }
 
 template <int kBytes>
@@ -383,10 +398,11 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
     const int piece_end = min(last, lin + cur.s.tiles - cur.tile);
     const bool whole = cur.tile == 0 && piece_end - lin == cur.s.tiles;
     // The unit's queries as B fragments: column g is row rt * 8 + g; the lane holds its dims that meet the words of a
-    // key row that it reads, paired as the codes are, in units of 2^-up.
+    // key row that it reads, paired as the codes are, in units of 2^-up (4 bits: second and fourth nibbles 2^(4 - up),
+    // as their codes are 2^4 larger).
     uint32_t qb[16];
-    float qsum[kGroups][2];  // per group, the sum of q over its dims, of columns 2 t and 2 t + 1
-    float down[2];           // softmax scale (log2 units) times 2^-up of columns 2 t and 2 t + 1
+    float qsum[kGroups][2];  // per group, the sum of q over its dims in units of 2^(24 - up), of columns 2 t and 2 t + 1
+    float down[2];           // softmax scale (log2 units) times 2^(24 - up) of columns 2 t and 2 t + 1
     {
       const int row = rt * 8 + g, i = row % p.Tq, h = cur.hk * G + row / p.Tq;
       const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128;
@@ -404,8 +420,8 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^up brings exponent `top` to 2^10 (an infinity or NaN stays one); 2^up and 2^-up are normal numbers
-      const int up = min(10 + 127 - static_cast<int>(top >> 7), 126);
+      // 2^up brings exponent `top` to 2^14 (an infinity or NaN stays one); 2^up and 2^-up are normal numbers
+      const int up = min(14 + 127 - static_cast<int>(top >> 7), 126);
       const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
       float part = 0.f;
 #pragma unroll
@@ -415,7 +431,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const float a = __uint_as_float(w[y] << 16) * mul, b = __uint_as_float(w[y] & 0xffff0000u) * mul;
-          f[y] = pack_f16x2(a, b);
+          f[y] = pack_f16x2(a, kBits == 4 ? b * 0.0625f : b);
           part += a + b;
         }
         if constexpr (kBits == 4) {  // dims (0,4) (1,5) (2,6) (3,7) of a word's eight
@@ -431,12 +447,12 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
           const int j = x / (kGroup / 32);
           part += __shfl_xor_sync(0xffffffffu, part, 1);
           part += __shfl_xor_sync(0xffffffffu, part, 2);
-          qsum[j][0] = __shfl_sync(0xffffffffu, part, 8 * t);
-          qsum[j][1] = __shfl_sync(0xffffffffu, part, 8 * t + 4);
+          qsum[j][0] = __shfl_sync(0xffffffffu, part, 8 * t) * 0x1p-24f;
+          qsum[j][1] = __shfl_sync(0xffffffffu, part, 8 * t + 4) * 0x1p-24f;
           part = 0.f;
         }
       }
-      const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+      const float back = (p.scale_log2 * 0x1p24f) * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
       down[0] = __shfl_sync(0xffffffffu, back, 8 * t);
       down[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
@@ -456,7 +472,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
         lds(sz[1], at + kp_lds + 8 * kGroups * 4);
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          float c[4];
           constexpr int kPart = kWords < 4 ? kWords : 4;  // words read at once
 #pragma unroll
           for (int w0 = 0; w0 < kWords; w0 += kPart) {
@@ -469,23 +485,25 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
               if constexpr (kBits == 4) {
                 const uint32_t* b = qb + 4 * (j * kWords + w0 + w);
                 uint32_t xa[4], xb[4];
-                centre4(xa, ka[w]);
-                centre4(xb, kb[w]);
-                mma_16x8x16(c, xa[0], xb[0], xa[1], xb[1], b[0], b[1]);
+                widen4<false>(xa, ka[w]);
+                widen4<false>(xb, kb[w]);
+                if (w0 + w == 0) mma_16x8x16_first(c, xa[0], xb[0], xa[1], xb[1], b[0], b[1]);
+                else mma_16x8x16(c, xa[0], xb[0], xa[1], xb[1], b[0], b[1]);
                 mma_16x8x16(c, xa[2], xb[2], xa[3], xb[3], b[2], b[3]);
               } else {
                 const uint32_t* b = qb + 2 * (j * kWords + w0 + w);
-                mma_16x8x16(c, centre8<0x0100>(ka[w]), centre8<0x0100>(kb[w]), centre8<0x0302>(ka[w]),
-                            centre8<0x0302>(kb[w]), b[0], b[1]);
+                const uint32_t a0 = widen8<false, 0x0100>(ka[w]), a1 = widen8<false, 0x0100>(kb[w]);
+                const uint32_t a2 = widen8<false, 0x0302>(ka[w]), a3 = widen8<false, 0x0302>(kb[w]);
+                if (w0 + w == 0) mma_16x8x16_first(c, a0, a1, a2, a3, b[0], b[1]);
+                else mma_16x8x16(c, a0, a1, a2, a3, b[0], b[1]);
               }
             }
           }
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float sc = __uint_as_float(sz[y][j] << 16);
-            const float zc = fmaf(kCentre, sc, __uint_as_float(sz[y][j] & 0xffff0000u));
+            const float sc = __uint_as_float(sz[y][j] << 16), z = __uint_as_float(sz[y][j] & 0xffff0000u);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) s[2 * y + e] = fmaf(sc, c[2 * y + e], fmaf(zc, qsum[j][e], s[2 * y + e]));
+            for (int e = 0; e < 2; ++e) s[2 * y + e] = fmaf(sc, c[2 * y + e], fmaf(z, qsum[j][e], s[2 * y + e]));
           }
         }
       }
@@ -586,8 +604,8 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
           if constexpr (kBits == 4) {
             const uint32_t sel = (kVWords < 1 ? g & 1 : r & 1) ? 0x7632u : 0x5410u;
             uint32_t x[4], y[4];
-            centre4(x, __byte_perm(va[r / 2], vb[r / 2], sel));
-            centre4(y, __byte_perm(vc[r / 2], vd[r / 2], sel));
+            widen4<true>(x, __byte_perm(va[r / 2], vb[r / 2], sel));
+            widen4<true>(y, __byte_perm(vc[r / 2], vd[r / 2], sel));
             mma_16x8x16(acc[j * kTiles + 2 * r], x[0], x[1], y[0], y[1], b[0], b[1]);
             mma_16x8x16(acc[j * kTiles + 2 * r + 1], x[2], x[3], y[2], y[3], b[0], b[1]);
           } else {
@@ -595,8 +613,8 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
             for (int h = 0; h < 2; ++h) {
               const uint32_t sel = h ? 0x7632u : 0x5410u;
               const uint32_t x = __byte_perm(va[r], vb[r], sel), y = __byte_perm(vc[r], vd[r], sel);
-              mma_16x8x16(acc[j * kTiles + 2 * r + h], centre8<0x0200>(x), centre8<0x0301>(x), centre8<0x0200>(y),
-                          centre8<0x0301>(y), b[0], b[1]);
+              mma_16x8x16(acc[j * kTiles + 2 * r + h], widen8<true, 0x0200>(x), widen8<true, 0x0301>(x),
+                          widen8<true, 0x0200>(y), widen8<true, 0x0301>(y), b[0], b[1]);
             }
           }
         }
@@ -626,9 +644,10 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
         for (int j = 0; j < kGroups; ++j) corr[j][c] += __shfl_xor_sync(0xffffffffu, corr[j][c], o);
       }
     }
-    float worth[kGroups];
+    float worth[kGroups];  // 2^24 of the codes, and what a weight's unit is
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) worth[j] = 1.f / unit[j];
+    for (int j = 0; j < kGroups; ++j) worth[j] = 0x1p24f / unit[j];
+    constexpr float kSecond = kBits == 4 ? 0.0625f : 1.f;  // rows g + 8 of a tile: second (fourth) nibbles
     __syncthreads();  // the previous piece's parts have been read
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -638,7 +657,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
       for (int i = 0; i < 8; ++i) {
         const int j = i / (kGroup / 16), dim = j * kGroup + g * (kGroup / 8) + 2 * (i % (kGroup / 16));
         *reinterpret_cast<float2*>(mg_o + col * 128 + dim) =
-            make_float2(fmaf(acc[i][c], worth[j], corr[j][c]), fmaf(acc[i][c + 2], worth[j], corr[j][c]));
+            make_float2(fmaf(acc[i][c], worth[j], corr[j][c]), fmaf(acc[i][c + 2] * kSecond, worth[j], corr[j][c]));
       }
       if (g == 0) *reinterpret_cast<float2*>(mg_ml + col * 2) = make_float2(m[c], l[c]);
     }
