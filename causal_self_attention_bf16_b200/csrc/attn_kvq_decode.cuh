@@ -26,10 +26,10 @@
 //   and the sums stay far from overflow): one vote a tile in place of the reduction and the rescaling.
 //
 // Work split. A unit is one (sequence, key/value head); its visible keys, tiles of 16. All units' tiles in a row are
-// dealt to the CTAs in equal stretches, found on the device from the lengths, so that every CTA reads the same
-// number of bytes however ragged the batch; a CTA's warps take its tiles in turn, through a ring of tiles in shared
-// memory that each warp fills for itself (cp.async; no barrier in the loop). A unit that ends in the CTA it began in
-// is finished there; one that spans CTAs leaves unnormalised pieces, which kvq_decode_merge_kernel joins.
+// dealt to the warps in equal stretches, found on the device from the lengths, so that every warp reads the same number
+// of bytes however ragged the batch, through a ring of tiles in shared memory that it fills for itself (cp.async; no
+// barrier in the loop). A unit that begins and ends in one warp's stretch is finished there; the pieces of one that
+// spans warps are joined by the CTA at its end, and the CTAs' pieces by kvq_decode_merge_kernel.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,7 +47,7 @@ __device__ uint32_t g_kvq_error;
 constexpr int kKvqMaxRows = 32;   // (H / H_kv) * Tq query rows per key/value head, at most
 constexpr int kKvqWarps = 8;      // warps per CTA
 constexpr int kKvqThreads = kKvqWarps * 32;
-constexpr int kKvqCtas = 2 * 148;  // CTAs of the split kernel, at most: two per SM
+constexpr int kKvqCtas = 2 * 148;  // CTAs of the split kernel, at most: two per SM of a 148-SM part
 constexpr int kKvqTile = 16;      // keys per tile
 
 enum : uint32_t {
@@ -59,8 +59,15 @@ enum : uint32_t {
 struct KvqSpan {
   int unit;      // b * H_kv + hk, or -1: none
   int last_cta;  // the CTA it ends in
-  int slot;      // this CTA's piece of it: 0 (its first stretch) or 1 (its last)
+  int slot;      // this CTA's piece of it: 0 if that has the CTA's first tile, else 1
   int pad;
+};
+
+// A warp's piece of a unit that does not both begin and end with it: its first one (slot 0) or its last (slot 1).
+struct KvqPiece {
+  int unit;    // b * H_kv + hk, or -1: none
+  int begins;  // the unit's first tile is the piece's
+  int end;     // the unit's end in the row of all tiles
 };
 
 struct KvqDecodeParams {
@@ -198,7 +205,10 @@ struct KvqShape {
   // Tiles per warp in the ring: one in use, the others in flight (4 bits: 2-2.5 KB a tile, 8 bits: 4-4.5 KB).
   static constexpr int kStages = kBits == 4 ? 3 : 2;
   static constexpr int kRing = kKvqWarps * kStages * kStageBytes;
-  static constexpr int kMerge = kKvqWarps * 8 * (128 + 2) * 4;  // 8 rows a warp
+  // Pieces to be joined: 8 rows a warp. The first is kept beside the ring, the last one takes its warp's ring over.
+  static constexpr int kPiece = 8 * 128 * 4;
+  static_assert(kPiece <= kStages * kStageBytes, "a piece fits a warp's ring");
+  static constexpr int kMerge = kKvqWarps * kPiece + 2 * kKvqWarps * 8 * 2 * 4;
   static constexpr int kSmem = kRing + kMerge;
 };
 
@@ -233,7 +243,7 @@ __device__ __forceinline__ void kvq_next_unit(const KvqDecodeParams& p, KvqCurso
 
 // ------------------------------------------------------------------------------------------------ split kernel
 
-// Warps take up to 8 query rows each: n_rt = ceil(R / 8) row tiles, and kKvqWarps / n_rt warps share the keys.
+// A warp takes up to 8 query rows; with more, n_rt = ceil(R / 8) warps take a stretch's tiles together.
 template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const KvqDecodeParams p) {
   using Shape = KvqShape<kBits, kGroup>;
@@ -243,8 +253,8 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
   constexpr float kNone = -3e38f;                // running max before the first key
   extern __shared__ __align__(128) uint8_t kvq_smem[];
-  __shared__ int sh_scan[kKvqWarps];
-  __shared__ int sh_b, sh_off;
+  __shared__ int sh_scan[kKvqWarps], sh_b[kKvqWarps], sh_off[kKvqWarps];
+  __shared__ KvqPiece sh_piece[2][kKvqWarps];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int R = p.R, G = p.H / p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge kernel waits for this grid's end)
@@ -260,6 +270,8 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
     if (lane >= d) incl += y;
   }
   if (lane == 31) sh_scan[warp] = incl;
+  if (tid < 2 * kKvqWarps) (&sh_piece[0][0])[tid].unit = -1;
+  if (tid == 0) p.spans[blockIdx.x].unit = -1;
   __syncthreads();
   int before = incl - sum, total = 0;
 #pragma unroll
@@ -267,22 +279,27 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
     if (w < warp) before += sh_scan[w];
     total += sh_scan[w];
   }
-  total *= p.Hkv;
+  total *= p.Hkv, before *= p.Hkv, sum *= p.Hkv;
   const int n_rt = (R + 7) / 8;
-  const int slices = kKvqWarps / n_rt;                  // warps that share the keys
-  const int share = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), slices);
-  const long long first64 = static_cast<long long>(blockIdx.x) * share;
-  const int first = first64 < total ? static_cast<int>(first64) : total;
-  const int last = static_cast<int>(min(static_cast<long long>(total), first64 + share));  // this CTA's tiles
-  if (first < last && before * p.Hkv <= first && first < (before + sum) * p.Hkv) {
-    int b = tid * per, at = before * p.Hkv;
-    for (;; ++b) {
-      const int n = kvq_seq(p, b).tiles * p.Hkv;
-      if (first < at + n) break;
-      at += n;
+  const int slices = kKvqWarps / n_rt;  // stretches per CTA, each for the n_rt warps of its row tiles
+  const int workers = static_cast<int>(gridDim.x) * slices;
+  const int share = (total + workers - 1) / workers;
+  // Stretch i of this CTA is tiles [start_of(i), start_of(i + 1)).
+  auto start_of = [&](int i) {
+    return static_cast<int>(min(static_cast<long long>(total), (static_cast<long long>(blockIdx.x) * slices + i) * share));
+  };
+  for (int i = 0; i < slices; ++i) {
+    const int at = start_of(i);
+    if (at < total && before <= at && at < before + sum) {  // one thread's: where stretch i begins
+      int b = tid * per, x = before;
+      for (;; ++b) {
+        const int n = kvq_seq(p, b).tiles * p.Hkv;
+        if (at < x + n) break;
+        x += n;
+      }
+      sh_b[i] = b;
+      sh_off[i] = at - x;
     }
-    sh_b = b;
-    sh_off = first - at;
   }
   // Sequences without keys: o = 0, lse = -inf, shared out over the CTAs.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -291,21 +308,20 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
     for (int i = tid; i < p.Tq * p.H * 16; i += kKvqThreads) o4[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i < p.Tq * p.H; i += kKvqThreads) p.lse[static_cast<size_t>(b) * p.Tq * p.H + i] = -INFINITY;
   }
-  if (first >= last) {
-    if (tid == 0) p.spans[blockIdx.x].unit = -1;
-    return;
-  }
+  if (start_of(0) >= total) return;
   __syncthreads();
 
-  KvqCursor cur;  // the unit being computed
-  cur.b = sh_b;
-  cur.s = kvq_seq(p, cur.b);
-  cur.hk = sh_off / cur.s.tiles;
-  cur.tile = sh_off % cur.s.tiles;
-  const int rt = warp % n_rt, slice = warp / n_rt;
-  const bool active = slice < slices;  // (three row tiles leave two warps over)
+  const int rt = warp % n_rt, slice = warp / n_rt;  // (three row tiles leave two warps over)
+  const int first = slice < slices ? start_of(slice) : total, last = slice < slices ? start_of(slice + 1) : total;
+  KvqCursor cur = {};  // the unit being computed
+  if (first < last) {
+    cur.b = sh_b[slice];
+    cur.s = kvq_seq(p, cur.b);
+    cur.hk = sh_off[slice] / cur.s.tiles;
+    cur.tile = sh_off[slice] % cur.s.tiles;
+  }
 
-  // --- the ring: this warp's tiles are slice, slice + slices, ... of the CTA's
+  // --- the ring
   const uint32_t ring = sm100::smem_u32(kvq_smem) + warp * kStages * Shape::kStageBytes;
   constexpr int kChunks = kRowBytes / 16, kRowsAtOnce = 32 / kChunks;  // 16-byte chunks of a row; rows a copy covers
   const int c_row = lane / kChunks, p_row = lane % 16;
@@ -319,8 +335,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   const size_t n_rows = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_rows;
   KvqCursor pre = cur;  // the next tile this warp fetches
-  pre.tile += slice;
-  int pre_lin = active ? first + slice : last;
+  int pre_lin = first;
   // its first row's codes at this lane's chunk, and its params (the lower half warp fetches the keys', the upper the
   // values')
   const uint8_t *k_from, *v_from, *p_from;
@@ -334,11 +349,9 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   };
   auto fetch = [&](int stage) {  // copies (or nothing) and one commit
     if (pre_lin < last) {
-      if (pre.tile >= pre.s.tiles) {
-        do {
-          pre.tile -= pre.s.tiles;
-          kvq_next_unit(p, pre);
-        } while (pre.tile >= pre.s.tiles);
+      if (pre.tile == pre.s.tiles) {
+        pre.tile = 0;
+        kvq_next_unit(p, pre);
         aim();
       }
       const int n = pre.s.L - (pre.s.start + pre.tile * kKvqTile);  // valid rows (at least one)
@@ -362,17 +375,16 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
         const bool in = p_row < n && ATTN_IN_RANGE(pre_row + p_row, 1, n_rows, kSiteKvqDecParams, &g_kvq_error);
         cp_async<kGroups * 4>(p_to, in ? p_from : reinterpret_cast<const uint8_t*>(p.k_params), in);
       }
-      const uint32_t rows = slices * kKvqTile;
-      pre_lin += slices;
-      pre.tile += slices;
-      pre_row += rows;
-      k_from += rows * kRowBytes;
-      v_from += rows * kRowBytes;
-      p_from += rows * (kGroups * 4);
+      ++pre_lin;
+      ++pre.tile;
+      pre_row += kKvqTile;
+      k_from += kKvqTile * kRowBytes;
+      v_from += kKvqTile * kRowBytes;
+      p_from += kKvqTile * kGroups * 4;
     }
     cp_async_commit();
   };
-  if (pre.tile < pre.s.tiles) aim();
+  aim();
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
@@ -386,17 +398,19 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   const uint32_t k_lds = at_byte(kg, t * kWords * 4), kp_lds = 2 * Shape::kCodeBytes + kg * kGroups * 4;
   const uint32_t v0_lds = Shape::kCodeBytes + at_byte(vk0, v_byte), v1_lds = Shape::kCodeBytes + at_byte(vk1, v_byte);
 
-  float* mg_o = reinterpret_cast<float*>(kvq_smem + Shape::kRing);        // [warp][column][128]
-  float* mg_ml = mg_o + kKvqWarps * 8 * 128;                             // [warp][column][2]
+  auto piece_o = [&](int slot, int w) {  // [8][128]
+    return reinterpret_cast<float*>(kvq_smem + (slot ? w * kStages * Shape::kStageBytes : Shape::kRing + w * Shape::kPiece));
+  };
+  auto piece_ml = [&](int slot, int w) {  // [8][2]
+    return reinterpret_cast<float*>(kvq_smem + Shape::kRing + kKvqWarps * Shape::kPiece) + (slot * kKvqWarps + w) * 16;
+  };
   const size_t n_q = static_cast<size_t>(p.B) * p.Tq * p.H * 128;
   (void)n_q;
 
   int stage = 0, lin = first;  // lin: first tile of the current piece
-  int mine = active ? first + slice : last;  // this warp's next tile
   while (lin < last) {
     // --- one piece: tiles [lin, piece_end) of unit (cur.b, cur.hk), from its tile cur.tile on
-    const int piece_end = min(last, lin + cur.s.tiles - cur.tile);
-    const bool whole = cur.tile == 0 && piece_end - lin == cur.s.tiles;
+    const int unit_end = lin - cur.tile + cur.s.tiles, piece_end = min(last, unit_end);
     // The unit's queries as B fragments: column g is row rt * 8 + g; the lane holds its dims that meet the words of a
     // key row that it reads, paired as the codes are, in units of 2^-up (4 bits: second and fourth nibbles 2^(4 - up),
     // as their codes are 2^4 larger).
@@ -621,8 +635,8 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
       }
     };
 
-    for (; mine < piece_end; mine += slices) {
-      const int key0 = cur.s.start + (cur.tile + mine - lin) * kKvqTile;
+    int key0 = cur.s.start + cur.tile * kKvqTile;
+    for (int n = piece_end - lin; n > 0; --n, key0 += kKvqTile) {
       cp_async_wait<kStages - 2>();
       __syncwarp();  // this tile is in, and every lane has read the one before it
       fetch(stage == 0 ? kStages - 1 : stage - 1);
@@ -634,7 +648,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
-    // --- the piece's result: the warps' parts, joined by their maxima
+    // --- the piece's result
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -648,62 +662,91 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) worth[j] = 0x1p24f / unit[j];
     constexpr float kSecond = kBits == 4 ? 0.0625f : 1.f;  // rows g + 8 of a tile: second (fourth) nibbles
-    __syncthreads();  // the previous piece's parts have been read
+    const bool whole = cur.tile == 0 && piece_end == unit_end;
+    const int slot = lin == first ? 0 : 1;
+    if (!whole && slot) __syncwarp();  // (every lane has read the last tile, which the piece overwrites)
+    float* to_o = piece_o(slot, warp);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int col = warp * 8 + 2 * t + c;
-      if (rt * 8 + 2 * t + c >= R) continue;
+      const int r = rt * 8 + 2 * t + c;
+      if (r >= R) continue;
+      const int i = r % p.Tq, h = cur.hk * G + r / p.Tq;
+      const float inv = l[c] == 0.f ? 0.f : 1.f / l[c];  // (a row that sees no key: 0)
+      const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = i / (kGroup / 16), dim = j * kGroup + g * (kGroup / 8) + 2 * (i % (kGroup / 16));
-        *reinterpret_cast<float2*>(mg_o + col * 128 + dim) =
-            make_float2(fmaf(acc[i][c], worth[j], corr[j][c]), fmaf(acc[i][c + 2] * kSecond, worth[j], corr[j][c]));
+      for (int x = 0; x < 8; ++x) {
+        const int j = x / (kGroup / 16), dim = j * kGroup + g * (kGroup / 8) + 2 * (x % (kGroup / 16));
+        const float a = fmaf(acc[x][c], worth[j], corr[j][c]);
+        const float b = fmaf(acc[x][c + 2] * kSecond, worth[j], corr[j][c]);
+        if (!whole)
+          *reinterpret_cast<float2*>(to_o + (2 * t + c) * 128 + dim) = make_float2(a, b);
+        else if (ATTN_IN_RANGE(off + dim, 2, n_q, kSiteKvqDecO, &g_kvq_error))
+          *reinterpret_cast<uint32_t*>(p.o + off + dim) = sm100::pack_bf16x2(a * inv, b * inv);
       }
-      if (g == 0) *reinterpret_cast<float2*>(mg_ml + col * 2) = make_float2(m[c], l[c]);
+      if (g) continue;
+      const size_t lse_i = (static_cast<size_t>(cur.b) * p.H + h) * p.Tq + i;
+      if (!whole)
+        *reinterpret_cast<float2*>(piece_ml(slot, warp) + (2 * t + c) * 2) = make_float2(m[c], l[c]);
+      else if (ATTN_IN_RANGE(lse_i, 1, n_q / 128, kSiteKvqDecLse, &g_kvq_error))
+        p.lse[lse_i] = l[c] == 0.f ? -INFINITY : (m[c] + log2f(l[c])) * 0.69314718055994531f;
     }
-    __syncthreads();
-    const int slot = lin == first ? 0 : 1;
-    for (int e = tid; e < R * 32; e += kKvqThreads) {
-      const int r = e / 32, d = (e % 32) * 4;
-      float M = kNone;
-      for (int s = 0; s < slices; ++s) M = fmaxf(M, mg_ml[((r / 8 + s * n_rt) * 8 + r % 8) * 2]);
-      float L = 0.f;
-      float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < slices; ++s) {
-        const int at = (r / 8 + s * n_rt) * 8 + r % 8;
-        const float f = ex2(mg_ml[at * 2] - M);
-        L = fmaf(mg_ml[at * 2 + 1], f, L);
-        const float4 x = *reinterpret_cast<const float4*>(mg_o + at * 128 + d);
-        o4.x = fmaf(x.x, f, o4.x), o4.y = fmaf(x.y, f, o4.y), o4.z = fmaf(x.z, f, o4.z), o4.w = fmaf(x.w, f, o4.w);
-      }
-      if (whole) {
-        const int i = r % p.Tq, h = cur.hk * G + r / p.Tq;
-        const float inv = L == 0.f ? 0.f : 1.f / L;  // (a row that sees no key: 0)
-        const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128 + d;
-        if (ATTN_IN_RANGE(off, 4, n_q, kSiteKvqDecO, &g_kvq_error))
-          *reinterpret_cast<uint2*>(p.o + off) =
-              make_uint2(sm100::pack_bf16x2(o4.x * inv, o4.y * inv), sm100::pack_bf16x2(o4.z * inv, o4.w * inv));
-        const size_t lse_i = (static_cast<size_t>(cur.b) * p.H + h) * p.Tq + i;
-        if (d == 0 && ATTN_IN_RANGE(lse_i, 1, n_q / 128, kSiteKvqDecLse, &g_kvq_error))
-          p.lse[lse_i] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-      } else {
-        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + slot) * R + r;
-        if (ATTN_IN_RANGE(part, 1, static_cast<size_t>(gridDim.x) * 2 * R, kSiteKvqDecPart, &g_kvq_error)) {
-          *reinterpret_cast<float4*>(p.part_o + part * 128 + d) = o4;
-          if (d == 0) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(M, L);
-        }
-      }
-    }
-    if (piece_end == last && tid == 0) {  // the last piece: does its unit begin here and go on?
-      const int end = lin - cur.tile + cur.s.tiles;  // the unit's end in the row of all tiles
-      const bool on = end > last && lin - cur.tile >= first;
-      p.spans[blockIdx.x] = KvqSpan{on ? cur.b * p.Hkv + cur.hk : -1, (end - 1) / share, slot, 0};
-    }
+    if (!whole && lane == 0 && rt == 0)
+      sh_piece[slot][slice] = KvqPiece{cur.b * p.Hkv + cur.hk, cur.tile == 0, unit_end};
     lin = piece_end;
     cur.tile = 0;
     if (lin < last) kvq_next_unit(p, cur);
   }
   cp_async_wait<0>();
+  __syncthreads();
+
+  // --- the CTA's pieces of one unit, joined by their maxima: a chain begins with a stretch's last piece, or with its
+  // first where the unit begins there (or the CTA does), and goes on through the first pieces of the stretches after it.
+  const int cta_end = start_of(slices);
+  for (int i = 0, n = 0; i < 2 * slices; ++i) {
+    const int s0 = i / 2, slot0 = i % 2;
+    const KvqPiece head = sh_piece[slot0][s0];
+    if (head.unit < 0 || !(slot0 || head.begins || s0 == 0)) continue;
+    int s1 = s0 + 1;  // the chain is head, then the first pieces of stretches s0 + 1 .. s1 - 1
+    while (s1 < slices && sh_piece[0][s1].unit == head.unit) ++s1;
+    const bool ends = head.end <= cta_end, whole = head.begins && ends;
+    const int cta_slot = i == 0 ? 0 : 1;
+    const int b = head.unit / p.Hkv, hk = head.unit % p.Hkv;
+    for (int r = (warp + 8 * kKvqMaxRows - n * R) % 8; r < R; r += 8) {  // rows of all chains in turn
+      auto at = [&](int s) { return s * n_rt + r / 8; };                 // the warp of stretch s that had row r
+      float M = piece_ml(slot0, at(s0))[(r % 8) * 2];
+      for (int s = s0 + 1; s < s1; ++s) M = fmaxf(M, piece_ml(0, at(s))[(r % 8) * 2]);
+      float L = 0.f;
+      float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = s0; s < s1; ++s) {
+        const int slot = s == s0 ? slot0 : 0;
+        const float2 ml = *reinterpret_cast<const float2*>(piece_ml(slot, at(s)) + (r % 8) * 2);
+        const float4 x = *reinterpret_cast<const float4*>(piece_o(slot, at(s)) + (r % 8) * 128 + lane * 4);
+        const float f = ex2(ml.x - M);
+        L = fmaf(ml.y, f, L);
+        o4.x = fmaf(x.x, f, o4.x), o4.y = fmaf(x.y, f, o4.y), o4.z = fmaf(x.z, f, o4.z), o4.w = fmaf(x.w, f, o4.w);
+      }
+      if (whole) {
+        const int q = r % p.Tq, h = hk * G + r / p.Tq;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const size_t off = ((static_cast<size_t>(b) * p.Tq + q) * p.H + h) * 128 + lane * 4;
+        if (ATTN_IN_RANGE(off, 4, n_q, kSiteKvqDecO, &g_kvq_error))
+          *reinterpret_cast<uint2*>(p.o + off) =
+              make_uint2(sm100::pack_bf16x2(o4.x * inv, o4.y * inv), sm100::pack_bf16x2(o4.z * inv, o4.w * inv));
+        const size_t lse_i = (static_cast<size_t>(b) * p.H + h) * p.Tq + q;
+        if (lane == 0 && ATTN_IN_RANGE(lse_i, 1, n_q / 128, kSiteKvqDecLse, &g_kvq_error))
+          p.lse[lse_i] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+      } else {
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + cta_slot) * R + r;
+        if (ATTN_IN_RANGE(part, 1, static_cast<size_t>(gridDim.x) * 2 * R, kSiteKvqDecPart, &g_kvq_error)) {
+          *reinterpret_cast<float4*>(p.part_o + part * 128 + lane * 4) = o4;
+          if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(M, L);
+        }
+      }
+      if (r == 0 && lane == 0 && head.begins && !ends)  // it begins here and goes on past this CTA
+        p.spans[blockIdx.x] = KvqSpan{head.unit, (head.end - 1) / (share * slices), cta_slot, 0};
+    }
+    ++n;
+  }
 }
 
 // ------------------------------------------------------------------------------------------------ merge kernel
