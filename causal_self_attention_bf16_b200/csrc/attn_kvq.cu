@@ -258,8 +258,8 @@ attn_status check_decode(int B, int H, int Hkv, int Tq, int Tk, int D, int bits,
   if (st != ATTN_OK) return st;
   if ((H / Hkv) * static_cast<long long>(Tq) > attn::kKvqMaxRows) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H * Tq > 0x7fffffffLL / 8) return ATTN_ERR_UNSUPPORTED;
-  // the units' 16-key tiles are counted in 31 bits
-  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL / (Tk / attn::kKvqTile + 1)) return ATTN_ERR_UNSUPPORTED;
+  // the units' tiles (16 keys or more) are counted in 31 bits
+  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL / (Tk / 16 + 1)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -268,10 +268,10 @@ int decode_span(int Tq, int Tk, int window) {
   return window < 0 ? Tk : static_cast<int>(std::min<long long>(Tk, static_cast<long long>(Tq) + window));
 }
 
-// CTAs of the split kernel: two per SM, or fewer where every warp of a CTA would not get a tile.
+// CTAs of the split kernel: one per SM, or fewer where every warp of a CTA would not get a 16-key tile.
 unsigned decode_grid(int B, int H, int Hkv, int Tq, int span) {
   const int R = (H / Hkv) * Tq, n_rt = (R + 7) / 8, slices = attn::kKvqWarps / n_rt;
-  const long long tiles = static_cast<long long>(B) * Hkv * ((span + attn::kKvqTile - 1) / attn::kKvqTile);
+  const long long tiles = static_cast<long long>(B) * Hkv * ((span + 15) / 16);
   return static_cast<unsigned>(std::min<long long>(attn::kKvqCtas, (tiles + slices - 1) / slices));
 }
 
@@ -284,7 +284,7 @@ template <int kBits, int kGroup>
 cudaError_t launch_split(const attn::KvqDecodeParams& p, unsigned ctas, cudaStream_t s) {
   auto kernel = attn::kvq_decode_split_kernel<kBits, kGroup>;
   constexpr int kSmem = attn::KvqShape<kBits, kGroup>::kSmem;
-  static_assert(2 * (kSmem + 1024 + 64) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kSmem + 1024 <= 227 * 1024, "one CTA per SM");
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   kernel<<<ctas, attn::kKvqThreads, kSmem, s>>>(p);

@@ -45,10 +45,9 @@ namespace attn {
 __device__ uint32_t g_kvq_error;
 
 constexpr int kKvqMaxRows = 32;   // (H / H_kv) * Tq query rows per key/value head, at most
-constexpr int kKvqWarps = 8;      // warps per CTA
+constexpr int kKvqWarps = 12;     // warps per CTA (divides by 1, 2, 3 and 4 row tiles)
 constexpr int kKvqThreads = kKvqWarps * 32;
-constexpr int kKvqCtas = 2 * 148;  // CTAs of the split kernel, at most: two per SM of a 148-SM part
-constexpr int kKvqTile = 16;      // keys per tile
+constexpr int kKvqCtas = 148;     // CTAs of the split kernel, at most: one per SM of a 148-SM part
 
 enum : uint32_t {
   kSiteKvqDecQ = 0xa4, kSiteKvqDecCodes = 0xa5, kSiteKvqDecParams = 0xa6, kSiteKvqDecO = 0xa7, kSiteKvqDecLse = 0xa8,
@@ -200,10 +199,11 @@ __device__ __forceinline__ int kvq_key(int g) { return ((g >> 1) & 1) | (((g ^ (
 template <int kBits, int kGroup>
 struct KvqShape {
   static constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
-  static constexpr int kCodeBytes = kKvqTile * kRowBytes, kParamBytes = kKvqTile * kGroups * 4;
+  static constexpr int kHalves = kBits == 4 ? 2 : 1, kTile = 16 * kHalves;  // keys per tile, 16 to a product
+  static constexpr int kCodeBytes = kTile * kRowBytes, kParamBytes = kTile * kGroups * 4;
   static constexpr int kStageBytes = 2 * kCodeBytes + 2 * kParamBytes;
-  // Tiles per warp in the ring: one in use, the others in flight (4 bits: 2-2.5 KB a tile, 8 bits: 4-4.5 KB).
-  static constexpr int kStages = kBits == 4 ? 3 : 2;
+  // Tiles per warp in the ring: one in use, the others in flight (4-5 KB a tile).
+  static constexpr int kStages = 2;
   static constexpr int kRing = kKvqWarps * kStages * kStageBytes;
   // Pieces to be joined: 8 rows a warp. The first is kept beside the ring, the last one takes its warp's ring over.
   static constexpr int kPiece = 8 * 128 * 4;
@@ -216,11 +216,12 @@ struct KvqShape {
 struct KvqSeq {
   int L, start, tiles;
 };
+template <int kTile>
 __device__ __forceinline__ KvqSeq kvq_seq(const KvqDecodeParams& p, int b) {
   KvqSeq s;
   s.L = min(max(p.seqlens[b], 0), p.Tk);  // lengths outside [0, Tk] are clamped
   s.start = p.window < 0 ? 0 : max(0, s.L - p.Tq - p.window);
-  s.tiles = (s.L - s.start + kKvqTile - 1) / kKvqTile;
+  s.tiles = (s.L - s.start + kTile - 1) / kTile;
   return s;
 }
 
@@ -229,6 +230,7 @@ struct KvqCursor {
   int b, hk, tile;
   KvqSeq s;
 };
+template <int kTile>
 __device__ __forceinline__ void kvq_next_unit(const KvqDecodeParams& p, KvqCursor& c) {
   if (++c.hk < p.Hkv) return;
   c.hk = 0;
@@ -237,7 +239,7 @@ __device__ __forceinline__ void kvq_next_unit(const KvqDecodeParams& p, KvqCurso
       c.s.tiles = 0x7fffffff;  // (past the last unit: never asked for)
       return;
     }
-    c.s = kvq_seq(p, c.b);
+    c.s = kvq_seq<kTile>(p, c.b);
   } while (c.s.tiles == 0);
 }
 
@@ -245,9 +247,10 @@ __device__ __forceinline__ void kvq_next_unit(const KvqDecodeParams& p, KvqCurso
 
 // A warp takes up to 8 query rows; with more, n_rt = ceil(R / 8) warps take a stretch's tiles together.
 template <int kBits, int kGroup>
-__global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const KvqDecodeParams p) {
+__global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const KvqDecodeParams p) {
   using Shape = KvqShape<kBits, kGroup>;
   constexpr int kGroups = Shape::kGroups, kRowBytes = Shape::kRowBytes, kStages = Shape::kStages;
+  constexpr int kHalves = Shape::kHalves, kTile = Shape::kTile;
   constexpr int kWords = kGroup * kBits / 128;   // 32-bit words of a key row and group that a lane scores
   constexpr int kVWords = kGroup * kBits / 256;  // words of a value row and group that a lane multiplies (0: half a word)
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   // Every sequence's tile count, summed: thread i takes sequences [i per, (i + 1) per).
   const int per = (p.B + kKvqThreads - 1) / kKvqThreads;
   int sum = 0;
-  for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) sum += kvq_seq(p, b).tiles;
+  for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) sum += kvq_seq<kTile>(p, b).tiles;
   int incl = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
     if (at < total && before <= at && at < before + sum) {  // one thread's: where stretch i begins
       int b = tid * per, x = before;
       for (;; ++b) {
-        const int n = kvq_seq(p, b).tiles * p.Hkv;
+        const int n = kvq_seq<kTile>(p, b).tiles * p.Hkv;
         if (at < x + n) break;
         x += n;
       }
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   }
   // Sequences without keys: o = 0, lse = -inf, shared out over the CTAs.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (kvq_seq(p, b).tiles > 0) continue;
+    if (kvq_seq<kTile>(p, b).tiles > 0) continue;
     uint4* o4 = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(b) * p.Tq * p.H * 128);
     for (int i = tid; i < p.Tq * p.H * 16; i += kKvqThreads) o4[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i < p.Tq * p.H; i += kKvqThreads) p.lse[static_cast<size_t>(b) * p.Tq * p.H + i] = -INFINITY;
@@ -311,12 +314,12 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   if (start_of(0) >= total) return;
   __syncthreads();
 
-  const int rt = warp % n_rt, slice = warp / n_rt;  // (three row tiles leave two warps over)
-  const int first = slice < slices ? start_of(slice) : total, last = slice < slices ? start_of(slice + 1) : total;
+  const int rt = warp % n_rt, slice = warp / n_rt;
+  const int first = start_of(slice), last = start_of(slice + 1);
   KvqCursor cur = {};  // the unit being computed
   if (first < last) {
     cur.b = sh_b[slice];
-    cur.s = kvq_seq(p, cur.b);
+    cur.s = kvq_seq<kTile>(p, cur.b);
     cur.hk = sh_off[slice] / cur.s.tiles;
     cur.tile = sh_off[slice] % cur.s.tiles;
   }
@@ -324,11 +327,11 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   // --- the ring
   const uint32_t ring = sm100::smem_u32(kvq_smem) + warp * kStages * Shape::kStageBytes;
   constexpr int kChunks = kRowBytes / 16, kRowsAtOnce = 32 / kChunks;  // 16-byte chunks of a row; rows a copy covers
-  const int c_row = lane / kChunks, p_row = lane % 16;
+  const int c_row = lane / kChunks, p_row = lane % 16;  // (params: 16 rows of keys by the lower lanes, of values by the upper)
   // (a copy's rows are a multiple of 4 apart, and of 8 where the swizzle looks at bit 2)
-  uint32_t code_at[kKvqTile / kRowsAtOnce];
+  uint32_t code_at[kTile / kRowsAtOnce];
 #pragma unroll
-  for (int i = 0; i < kKvqTile / kRowsAtOnce; ++i) {
+  for (int i = 0; i < kTile / kRowsAtOnce; ++i) {
     const int r = c_row + i * kRowsAtOnce;
     code_at[i] = r * kRowBytes + (((lane % kChunks) ^ kvq_swizzle<kBits>(r)) << 4);
   }
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
   const uint8_t *k_from, *v_from, *p_from;
   size_t pre_row;
   auto aim = [&]() {
-    pre_row = (static_cast<size_t>(pre.b) * p.Hkv + pre.hk) * p.Tk + (pre.s.start + pre.tile * kKvqTile);
+    pre_row = (static_cast<size_t>(pre.b) * p.Hkv + pre.hk) * p.Tk + (pre.s.start + pre.tile * kTile);
     k_from = p.k_codes + pre_row * kRowBytes + lane * 16;
     v_from = p.v_codes + pre_row * kRowBytes + lane * 16;
     p_from = reinterpret_cast<const uint8_t*>(lane < 16 ? p.k_params : p.v_params) +
@@ -351,36 +354,42 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
     if (pre_lin < last) {
       if (pre.tile == pre.s.tiles) {
         pre.tile = 0;
-        kvq_next_unit(p, pre);
+        kvq_next_unit<kTile>(p, pre);
         aim();
       }
-      const int n = pre.s.L - (pre.s.start + pre.tile * kKvqTile);  // valid rows (at least one)
+      const int n = pre.s.L - (pre.s.start + pre.tile * kTile);  // valid rows (at least one)
       const uint32_t to = ring + stage * Shape::kStageBytes;
-      const uint32_t p_to = to + 2 * Shape::kCodeBytes + lane * kGroups * 4;
-      if (n >= kKvqTile && ATTN_IN_RANGE(pre_row, kKvqTile, n_rows, kSiteKvqDecCodes, &g_kvq_error)) {
+      const uint32_t p_to = to + 2 * Shape::kCodeBytes + (lane < 16 ? 0 : Shape::kParamBytes) + p_row * kGroups * 4;
+      if (n >= kTile && ATTN_IN_RANGE(pre_row, kTile, n_rows, kSiteKvqDecCodes, &g_kvq_error)) {
 #pragma unroll
-        for (int i = 0; i < kKvqTile / kRowsAtOnce; ++i) {
+        for (int i = 0; i < kTile / kRowsAtOnce; ++i) {
           cp_async<16>(to + code_at[i], k_from + i * 512);
           cp_async<16>(to + code_at[i] + Shape::kCodeBytes, v_from + i * 512);
         }
-        cp_async<kGroups * 4>(p_to, p_from);
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) cp_async<kGroups * 4>(p_to + i * 64 * kGroups, p_from + i * 64 * kGroups);
       } else {  // rows past the sequence's end are zeros, and not read
 #pragma unroll
-        for (int i = 0; i < kKvqTile / kRowsAtOnce; ++i) {
+        for (int i = 0; i < kTile / kRowsAtOnce; ++i) {
           const int r = c_row + i * kRowsAtOnce;
           const bool in = r < n && ATTN_IN_RANGE(pre_row + r, 1, n_rows, kSiteKvqDecCodes, &g_kvq_error);
           cp_async<16>(to + code_at[i], in ? k_from + i * 512 : p.k_codes, in);
           cp_async<16>(to + code_at[i] + Shape::kCodeBytes, in ? v_from + i * 512 : p.v_codes, in);
         }
-        const bool in = p_row < n && ATTN_IN_RANGE(pre_row + p_row, 1, n_rows, kSiteKvqDecParams, &g_kvq_error);
-        cp_async<kGroups * 4>(p_to, in ? p_from : reinterpret_cast<const uint8_t*>(p.k_params), in);
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) {
+          const int r = p_row + 16 * i;
+          const bool in = r < n && ATTN_IN_RANGE(pre_row + r, 1, n_rows, kSiteKvqDecParams, &g_kvq_error);
+          cp_async<kGroups * 4>(p_to + i * 64 * kGroups,
+                                in ? p_from + i * 64 * kGroups : reinterpret_cast<const uint8_t*>(p.k_params), in);
+        }
       }
       ++pre_lin;
       ++pre.tile;
-      pre_row += kKvqTile;
-      k_from += kKvqTile * kRowBytes;
-      v_from += kKvqTile * kRowBytes;
-      p_from += kKvqTile * kGroups * 4;
+      pre_row += kTile;
+      k_from += kTile * kRowBytes;
+      v_from += kTile * kRowBytes;
+      p_from += kTile * kGroups * 4;
     }
     cp_async_commit();
   };
@@ -471,26 +480,29 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
       down[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
     float acc[8][4], corr[kGroups][2], m[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
-    float unit[kGroups], most[kGroups];  // value weights are in units of 1 / unit; most: the largest scale that fits
+    float unit[kGroups];  // value weights are in units of 1 / unit, a power of two
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = most[j] = 0.f, unit[j] = 1.f;
+    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = 0.f, unit[j] = 0x1p127f;
 
     auto tile = [&](const uint32_t at, const int key0, auto masked) {
-      // --- scores: rows g and g + 8 are keys kg and kg + 8
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      {
+      // --- scores: rows g and g + 8 of half y are keys kg + 16 y and kg + 16 y + 8
+      float s[4 * kHalves];
+#pragma unroll
+      for (int y = 0; y < kHalves; ++y) {
         uint32_t sz[2][kGroups];
-        lds(sz[0], at + kp_lds);
-        lds(sz[1], at + kp_lds + 8 * kGroups * 4);
+        lds(sz[0], at + kp_lds + 16 * y * kGroups * 4);
+        lds(sz[1], at + kp_lds + (16 * y + 8) * kGroups * 4);
+        float* sy = s + 4 * y;
+        sy[0] = sy[1] = sy[2] = sy[3] = 0.f;
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
           float c[4];
           constexpr int kPart = kWords < 4 ? kWords : 4;  // words read at once
 #pragma unroll
           for (int w0 = 0; w0 < kWords; w0 += kPart) {
-            const uint32_t a = (at + k_lds) ^ (j * (kGroup * kBits / 8) + w0 * 4);
+            const uint32_t a = ((at + k_lds) ^ (j * (kGroup * kBits / 8) + w0 * 4)) + 16 * y * kRowBytes;
             uint32_t ka[kPart], kb[kPart];
             lds(ka, a);
             lds(kb, a + 8 * kRowBytes);
@@ -514,45 +526,52 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
             }
           }
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float sc = __uint_as_float(sz[y][j] << 16), z = __uint_as_float(sz[y][j] & 0xffff0000u);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s[2 * y + e] = fmaf(sc, c[2 * y + e], fmaf(z, qsum[j][e], s[2 * y + e]));
-          }
+          for (int e = 0; e < 4; ++e)
+            sy[e] = fmaf(__uint_as_float(sz[e / 2][j] << 16), c[e],
+                         fmaf(__uint_as_float(sz[e / 2][j] & 0xffff0000u), qsum[j][e & 1], sy[e]));
         }
       }
       // --- softmax: keys past a row's last (or before its window) have weight 0, whatever they hold
-      uint32_t vsz[2][kGroups];
-      lds(vsz[0], at + kp_lds + Shape::kParamBytes);
-      lds(vsz[1], at + kp_lds + Shape::kParamBytes + 8 * kGroups * 4);
-      bool seen[4] = {true, true, true, true};
-      if constexpr (masked.value) {
+      bool seen[4 * kHalves];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 4 * kHalves; ++e) {
+        seen[e] = true;
+        if constexpr (masked.value) {
           const int key = key0 + kg + 8 * (e / 2), hi = cur.s.L - p.Tq + (rt * 8 + 2 * t + (e & 1)) % p.Tq;
           seen[e] = key <= hi && (p.window < 0 || key >= hi - p.window);
         }
       }
-      float x[4];  // log2 of the weights
+      float x[4 * kHalves];  // log2 of the weights
+      bool raise = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = seen[e] ? fmaf(s[e], down[e & 1], -m[e & 1]) : -INFINITY;
-      bool raise = x[0] > 8.f || x[1] > 8.f || x[2] > 8.f || x[3] > 8.f;
+      for (int e = 0; e < 4 * kHalves; ++e) {
+        x[e] = seen[e] ? fmaf(s[e], down[e & 1], -m[e & 1]) : -INFINITY;
+        raise |= x[e] > 8.f;
+      }
+      uint32_t vsz[2 * kHalves][kGroups];
 #pragma unroll
-      for (int j = 0; j < kGroups; ++j)
-        raise = raise || __uint_as_float(vsz[0][j] << 16) > most[j] || __uint_as_float(vsz[1][j] << 16) > most[j];
+      for (int y = 0; y < 2 * kHalves; ++y) lds(vsz[y], at + kp_lds + Shape::kParamBytes + 8 * y * kGroups * 4);
+      float top[kGroups];  // the largest scale of this lane's keys
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        top[j] = __uint_as_float(vsz[0][j] << 16);
+#pragma unroll
+        for (int y = 1; y < 2 * kHalves; ++y) top[j] = fmaxf(top[j], __uint_as_float(vsz[y][j] << 16));
+        raise |= top[j] * unit[j] > 64.f;
+      }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float y = m[c];  // the new max
 #pragma unroll
-          for (int e = c; e < 4; e += 2)
+          for (int e = c; e < 4 * kHalves; e += 2)
             if (seen[e]) y = fmaxf(y, s[e] * down[c]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
           const float f = ex2(m[c] - y);
           m[c] = y;
 #pragma unroll
-          for (int e = c; e < 4; e += 2)
+          for (int e = c; e < 4 * kHalves; e += 2)
             if (seen[e]) x[e] = fmaf(s[e], down[c], -y);
           l[c] *= f;
 #pragma unroll
@@ -562,86 +581,90 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
         }
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
-          float y = fmaxf(__uint_as_float(vsz[0][j] << 16), __uint_as_float(vsz[1][j] << 16));
+          float y = top[j];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-          if (y > most[j]) {
-            const int e = max(static_cast<int>(__float_as_uint(y) >> 23), 1);  // exponent field of the largest scale
-            const float to = __uint_as_float(static_cast<uint32_t>(max(254 - e, 1)) << 23);  // 2^-(e - 127)
-            const float f = most[j] == 0.f ? 0.f : to / unit[j];  // (no sums yet: they are 0)
+          if (y * unit[j] > 64.f) {  // the unit becomes the largest scale's power of two
+            const int e = static_cast<int>(__float_as_uint(y) >> 23);  // its exponent field
+            const float to = __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 1), 254)) << 23);
+            const float f = to / unit[j];
             unit[j] = to;
-            most[j] = __uint_as_float(static_cast<uint32_t>(min(e + 5, 254)) << 23);
 #pragma unroll
             for (int i = j * (kGroup / 16); i < (j + 1) * (kGroup / 16); ++i)
               acc[i][0] *= f, acc[i][1] *= f, acc[i][2] *= f, acc[i][3] *= f;
           }
         }
       }
-      float pr[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pr[e] = ex2(x[e]);
-      l[0] += pr[0] + pr[2];
-      l[1] += pr[1] + pr[3];
+      for (int e = 0; e < 4 * kHalves; ++e) {
+        x[e] = ex2(x[e]);
+        l[e & 1] += x[e];
+      }
       // --- values
 #pragma unroll
-      for (int j = 0; j < kGroups; ++j) {
-        uint32_t b[2];  // the weights of keys kg (+ 8) and columns 2 t, 2 t + 1, then transposed
+      for (int y = 0; y < kHalves; ++y) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float sc = __uint_as_float(vsz[y][j] << 16);
-          const float zc = fmaf(kCentre, sc, __uint_as_float(vsz[y][j] & 0xffff0000u));
-          const float su = sc * unit[j];
-          float w0 = pr[2 * y] * su, w1 = pr[2 * y + 1] * su;
-          if constexpr (masked.value) {  // (a NaN in a key that a row does not see stays out of it)
-            if (!seen[2 * y]) w0 = 0.f;
-            if (!seen[2 * y + 1]) w1 = 0.f;
-            if (seen[2 * y]) corr[j][0] = fmaf(pr[2 * y], zc, corr[j][0]);
-            if (seen[2 * y + 1]) corr[j][1] = fmaf(pr[2 * y + 1], zc, corr[j][1]);
-          } else {
-            corr[j][0] = fmaf(pr[2 * y], zc, corr[j][0]);
-            corr[j][1] = fmaf(pr[2 * y + 1], zc, corr[j][1]);
+        for (int j = 0; j < kGroups; ++j) {
+          uint32_t b[2];  // the weights of keys kg (+ 8) and columns 2 t, 2 t + 1, then transposed
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int e = 4 * y + 2 * z;
+            const uint32_t w = vsz[2 * y + z][j];
+            const float sc = __uint_as_float(w << 16), zc = fmaf(kCentre, sc, __uint_as_float(w & 0xffff0000u));
+            const float su = sc * unit[j];
+            float w0 = x[e] * su, w1 = x[e + 1] * su;
+            if constexpr (masked.value) {  // (a NaN in a key that a row does not see stays out of it)
+              if (!seen[e]) w0 = 0.f;
+              if (!seen[e + 1]) w1 = 0.f;
+              if (seen[e]) corr[j][0] = fmaf(x[e], zc, corr[j][0]);
+              if (seen[e + 1]) corr[j][1] = fmaf(x[e + 1], zc, corr[j][1]);
+            } else {
+              corr[j][0] = fmaf(x[e], zc, corr[j][0]);
+              corr[j][1] = fmaf(x[e + 1], zc, corr[j][1]);
+            }
+            b[z] = movmatrix(pack_f16x2(w0, w1));
           }
-          b[y] = movmatrix(pack_f16x2(w0, w1));
-        }
-        // The lane's dims j * kGroup + g * (kGroup / 8) + ... of its four keys: eight dims a word (4 bits) or four (8
-        // bits); with 4 bits and groups of 32 the lane's four dims are half a word.
-        constexpr int kRead = kVWords < 1 ? 1 : kVWords;
-        const uint32_t a0 = (at + v0_lds) ^ (j * (kGroup * kBits / 8)), a1 = (at + v1_lds) ^ (j * (kGroup * kBits / 8));
-        uint32_t va[kRead], vb[kRead], vc[kRead], vd[kRead];
-        lds(va, a0);
-        lds(vb, a1);
-        lds(vc, a0 + 8 * kRowBytes);
-        lds(vd, a1 + 8 * kRowBytes);
-        constexpr int kTiles = kGroup / 16;  // tiles of 16 dims in the group
+          // The lane's dims j * kGroup + g * (kGroup / 8) + ... of its four keys: eight dims a word (4 bits) or four (8
+          // bits); with 4 bits and groups of 32 the lane's four dims are half a word.
+          constexpr int kRead = kVWords < 1 ? 1 : kVWords;
+          const uint32_t a0 = ((at + v0_lds) ^ (j * (kGroup * kBits / 8))) + 16 * y * kRowBytes;
+          const uint32_t a1 = ((at + v1_lds) ^ (j * (kGroup * kBits / 8))) + 16 * y * kRowBytes;
+          uint32_t va[kRead], vb[kRead], vc[kRead], vd[kRead];
+          lds(va, a0);
+          lds(vb, a1);
+          lds(vc, a0 + 8 * kRowBytes);
+          lds(vd, a1 + 8 * kRowBytes);
+          constexpr int kTiles = kGroup / 16;  // tiles of 16 dims in the group
 #pragma unroll
-        for (int r = 0; r < kGroup / 32; ++r) {  // four dims at a time
-          if constexpr (kBits == 4) {
-            const uint32_t sel = (kVWords < 1 ? g & 1 : r & 1) ? 0x7632u : 0x5410u;
-            uint32_t x[4], y[4];
-            widen4<true>(x, __byte_perm(va[r / 2], vb[r / 2], sel));
-            widen4<true>(y, __byte_perm(vc[r / 2], vd[r / 2], sel));
-            mma_16x8x16(acc[j * kTiles + 2 * r], x[0], x[1], y[0], y[1], b[0], b[1]);
-            mma_16x8x16(acc[j * kTiles + 2 * r + 1], x[2], x[3], y[2], y[3], b[0], b[1]);
-          } else {
+          for (int r = 0; r < kGroup / 32; ++r) {  // four dims at a time
+            if constexpr (kBits == 4) {
+              const uint32_t sel = (kVWords < 1 ? g & 1 : r & 1) ? 0x7632u : 0x5410u;
+              uint32_t u[4], v[4];
+              widen4<true>(u, __byte_perm(va[r / 2], vb[r / 2], sel));
+              widen4<true>(v, __byte_perm(vc[r / 2], vd[r / 2], sel));
+              mma_16x8x16(acc[j * kTiles + 2 * r], u[0], u[1], v[0], v[1], b[0], b[1]);
+              mma_16x8x16(acc[j * kTiles + 2 * r + 1], u[2], u[3], v[2], v[3], b[0], b[1]);
+            } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t sel = h ? 0x7632u : 0x5410u;
-              const uint32_t x = __byte_perm(va[r], vb[r], sel), y = __byte_perm(vc[r], vd[r], sel);
-              mma_16x8x16(acc[j * kTiles + 2 * r + h], widen8<true, 0x0200>(x), widen8<true, 0x0301>(x),
-                          widen8<true, 0x0200>(y), widen8<true, 0x0301>(y), b[0], b[1]);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = h ? 0x7632u : 0x5410u;
+                const uint32_t u = __byte_perm(va[r], vb[r], sel), v = __byte_perm(vc[r], vd[r], sel);
+                mma_16x8x16(acc[j * kTiles + 2 * r + h], widen8<true, 0x0200>(u), widen8<true, 0x0301>(u),
+                            widen8<true, 0x0200>(v), widen8<true, 0x0301>(v), b[0], b[1]);
+              }
             }
           }
         }
       }
     };
 
-    int key0 = cur.s.start + cur.tile * kKvqTile;
-    for (int n = piece_end - lin; n > 0; --n, key0 += kKvqTile) {
+    int key0 = cur.s.start + cur.tile * kTile;
+    for (int n = piece_end - lin; n > 0; --n, key0 += kTile) {
       cp_async_wait<kStages - 2>();
       __syncwarp();  // this tile is in, and every lane has read the one before it
       fetch(stage == 0 ? kStages - 1 : stage - 1);
       const uint32_t at = ring + stage * Shape::kStageBytes;
-      if (key0 + kKvqTile - 1 <= cur.s.L - p.Tq && (p.window < 0 || key0 >= cur.s.L - 1 - p.window))
+      if (key0 + kTile - 1 <= cur.s.L - p.Tq && (p.window < 0 || key0 >= cur.s.L - 1 - p.window))
         tile(at, key0, std::false_type());  // every row sees every key
       else
         tile(at, key0, std::true_type());
@@ -694,7 +717,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
       sh_piece[slot][slice] = KvqPiece{cur.b * p.Hkv + cur.hk, cur.tile == 0, unit_end};
     lin = piece_end;
     cur.tile = 0;
-    if (lin < last) kvq_next_unit(p, cur);
+    if (lin < last) kvq_next_unit<kTile>(p, cur);
   }
   cp_async_wait<0>();
   __syncthreads();
@@ -711,7 +734,7 @@ __global__ void __launch_bounds__(kKvqThreads, 2) kvq_decode_split_kernel(const 
     const bool ends = head.end <= cta_end, whole = head.begins && ends;
     const int cta_slot = i == 0 ? 0 : 1;
     const int b = head.unit / p.Hkv, hk = head.unit % p.Hkv;
-    for (int r = (warp + 8 * kKvqMaxRows - n * R) % 8; r < R; r += 8) {  // rows of all chains in turn
+    for (int r = (warp + 64 * kKvqWarps - n * R) % kKvqWarps; r < R; r += kKvqWarps) {  // rows of all chains in turn
       auto at = [&](int s) { return s * n_rt + r / 8; };                 // the warp of stretch s that had row r
       float M = piece_ml(slot0, at(s0))[(r % 8) * 2];
       for (int s = s0 + 1; s < s1; ++s) M = fmaxf(M, piece_ml(0, at(s))[(r % 8) * 2]);
