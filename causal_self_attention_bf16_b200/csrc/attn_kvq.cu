@@ -258,8 +258,8 @@ attn_status check_decode(int B, int H, int Hkv, int Tq, int Tk, int D, int bits,
   if (st != ATTN_OK) return st;
   if ((H / Hkv) * static_cast<long long>(Tq) > attn::kKvqMaxRows) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H * Tq > 0x7fffffffLL / 8) return ATTN_ERR_UNSUPPORTED;
-  // the units' tiles (16 keys or more) are counted in 31 bits
-  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL / (Tk / 16 + 1)) return ATTN_ERR_UNSUPPORTED;
+  // the units' tiles (16 keys or more) are counted in 30 bits
+  if (static_cast<long long>(B) * Hkv > (1LL << 30) / (Tk / 16 + 1)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -395,6 +395,7 @@ attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_pa
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
   const int R = p.R = (H / H_kv) * Tq;
+  for (int r = 0; r < attn::kKvqMaxRows; ++r) p.row_i[r] = r < R ? r % Tq : 0, p.row_g[r] = r < R ? r / Tq : 0;
   const unsigned ctas = decode_grid(B, H, H_kv, Tq, decode_span(Tq, Tk, window));
   // (laid out for the most CTAs, those without a window)
   const size_t most = decode_grid(B, H, H_kv, Tq, Tk);

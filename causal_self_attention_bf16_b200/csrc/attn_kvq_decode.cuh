@@ -84,6 +84,7 @@ struct KvqDecodeParams {
   int B, H, Hkv, Tq, Tk, R;
   int window;                    // sliding window: the query at position p sees keys p - window .. p; -1: none
   float scale_log2;              // scale * log2(e)
+  uint8_t row_i[kKvqMaxRows], row_g[kKvqMaxRows];  // row r is token r % Tq of query head r / Tq of the group
 };
 
 // ------------------------------------------------------------------------------------------------ fragments
@@ -111,6 +112,17 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// lse of a row from its max m and sum l (log2 units), o's factor from its sum; a row that saw no key has l = 0.
+__device__ __forceinline__ float kvq_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+}
+__device__ __forceinline__ float kvq_factor(float l) { return l == 0.f ? 0.f : rcp(l); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -182,6 +194,9 @@ __device__ __forceinline__ void lds(uint32_t (&w)[kWords], uint32_t addr) {
                    : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(addr + 4 * i));
   }
 }
+
+// 1 / x of a power of two in [2^-126, 2^126].
+__device__ __forceinline__ float kvq_inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // ------------------------------------------------------------------------------------------------ layout
 
@@ -256,72 +271,56 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
   constexpr float kNone = -3e38f;                // running max before the first key
   extern __shared__ __align__(128) uint8_t kvq_smem[];
-  __shared__ int sh_scan[kKvqWarps], sh_b[kKvqWarps], sh_off[kKvqWarps];
-  __shared__ KvqPiece sh_piece[2][kKvqWarps];
+  __shared__ KvqPiece sh_piece[2 * kKvqWarps];  // stretch i's slots at 2 i, 2 i + 1
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int R = p.R, G = p.H / p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge kernel waits for this grid's end)
-
-  // Every sequence's tile count, summed: thread i takes sequences [i per, (i + 1) per).
-  const int per = (p.B + kKvqThreads - 1) / kKvqThreads;
-  int sum = 0;
-  for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) sum += kvq_seq<kTile>(p, b).tiles;
-  int incl = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += y;
-  }
-  if (lane == 31) sh_scan[warp] = incl;
-  if (tid < 2 * kKvqWarps) (&sh_piece[0][0])[tid].unit = -1;
   if (tid == 0) p.spans[blockIdx.x].unit = -1;
-  __syncthreads();
-  int before = incl - sum, total = 0;
-#pragma unroll
-  for (int w = 0; w < kKvqWarps; ++w) {
-    if (w < warp) before += sh_scan[w];
-    total += sh_scan[w];
+
+  // All units' tiles, then where this warp's stretch of them begins: every warp looks for itself, 32 sequences at a
+  // time.
+  int total = 0;
+  bool empty = false;  // whether there are sequences without keys
+  for (int b = lane; b < p.B; b += 32) {
+    const int n = kvq_seq<kTile>(p, b).tiles;
+    total += n;
+    empty |= n == 0;
   }
-  total *= p.Hkv, before *= p.Hkv, sum *= p.Hkv;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  total *= p.Hkv;
   const int n_rt = (R + 7) / 8;
   const int slices = kKvqWarps / n_rt;  // stretches per CTA, each for the n_rt warps of its row tiles
-  const int workers = static_cast<int>(gridDim.x) * slices;
-  const int share = (total + workers - 1) / workers;
+  const int rt = warp % n_rt, slice = warp / n_rt;
+  if (rt == 0 && lane < 2) sh_piece[2 * slice + lane].unit = -1;  // (this warp's to write; read after the barrier)
+  const int share = (total + static_cast<int>(gridDim.x) * slices - 1) / (static_cast<int>(gridDim.x) * slices);
   // Stretch i of this CTA is tiles [start_of(i), start_of(i + 1)).
   auto start_of = [&](int i) {
     return static_cast<int>(min(static_cast<long long>(total), (static_cast<long long>(blockIdx.x) * slices + i) * share));
   };
-  for (int i = 0; i < slices; ++i) {
-    const int at = start_of(i);
-    if (at < total && before <= at && at < before + sum) {  // one thread's: where stretch i begins
-      int b = tid * per, x = before;
-      for (;; ++b) {
-        const int n = kvq_seq<kTile>(p, b).tiles * p.Hkv;
-        if (at < x + n) break;
-        x += n;
-      }
-      sh_b[i] = b;
-      sh_off[i] = at - x;
-    }
-  }
-  // Sequences without keys: o = 0, lse = -inf, shared out over the CTAs.
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (kvq_seq<kTile>(p, b).tiles > 0) continue;
-    uint4* o4 = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(b) * p.Tq * p.H * 128);
-    for (int i = tid; i < p.Tq * p.H * 16; i += kKvqThreads) o4[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = tid; i < p.Tq * p.H; i += kKvqThreads) p.lse[static_cast<size_t>(b) * p.Tq * p.H + i] = -INFINITY;
-  }
-  if (start_of(0) >= total) return;
-  __syncthreads();
-
-  const int rt = warp % n_rt, slice = warp / n_rt;
   const int first = start_of(slice), last = start_of(slice + 1);
   KvqCursor cur = {};  // the unit being computed
   if (first < last) {
-    cur.b = sh_b[slice];
-    cur.s = kvq_seq<kTile>(p, cur.b);
-    cur.hk = sh_off[slice] / cur.s.tiles;
-    cur.tile = sh_off[slice] % cur.s.tiles;
+    for (int b0 = 0, before = 0;; b0 += 32) {
+      const int b = b0 + lane, n = b < p.B ? kvq_seq<kTile>(p, b).tiles * p.Hkv : 0;
+      int incl = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + incl > first);
+      if (past) {  // (some sequence ends past it: first < total)
+        const int l = __ffs(past) - 1;
+        cur.b = b0 + l;
+        cur.s = kvq_seq<kTile>(p, cur.b);
+        const int off = first - (before + __shfl_sync(0xffffffffu, incl - n, l));
+        cur.hk = off / cur.s.tiles;
+        cur.tile = off - cur.hk * cur.s.tiles;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
   }
 
   // --- the ring
@@ -404,7 +403,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   auto at_byte = [](int row, int byte) {
     return row * kRowBytes + (((byte >> 4) ^ kvq_swizzle<kBits>(row)) << 4) + (byte & 15);
   };
-  const uint32_t k_lds = at_byte(kg, t * kWords * 4), kp_lds = 2 * Shape::kCodeBytes + kg * kGroups * 4;
+  const uint32_t k_lds = at_byte(kg, t * kWords * 4), kp_lds = kg * kGroups * 4;
   const uint32_t v0_lds = Shape::kCodeBytes + at_byte(vk0, v_byte), v1_lds = Shape::kCodeBytes + at_byte(vk1, v_byte);
 
   auto piece_o = [&](int slot, int w) {  // [8][128]
@@ -427,7 +426,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
     float qsum[kGroups][2];  // per group, the sum of q over its dims in units of 2^(24 - up), of columns 2 t and 2 t + 1
     float down[2];           // softmax scale (log2 units) times 2^(24 - up) of columns 2 t and 2 t + 1
     {
-      const int row = rt * 8 + g, i = row % p.Tq, h = cur.hk * G + row / p.Tq;
+      const int row = rt * 8 + g, i = p.row_i[row], h = cur.hk * G + p.row_g[row];
       const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128;
       const bool live = row < R && ATTN_IN_RANGE(off, 128, n_q, kSiteKvqDecQ, &g_kvq_error);
       uint4 u[4];
@@ -484,16 +483,18 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = 0.f, unit[j] = 0x1p127f;
+    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = 0.f, unit[j] = 0x1p126f;
 
-    auto tile = [&](const uint32_t at, const int key0, auto masked) {
+    // The tile of codes at `at` and params at `ap`: n_halves times 16 keys, from key0 on.
+    auto tile = [&](const uint32_t at, const uint32_t ap, const int key0, auto masked, auto n_halves) {
+      constexpr int kN = n_halves.value;
       // --- scores: rows g and g + 8 of half y are keys kg + 16 y and kg + 16 y + 8
-      float s[4 * kHalves];
+      float s[4 * kN];
 #pragma unroll
-      for (int y = 0; y < kHalves; ++y) {
+      for (int y = 0; y < kN; ++y) {
         uint32_t sz[2][kGroups];
-        lds(sz[0], at + kp_lds + 16 * y * kGroups * 4);
-        lds(sz[1], at + kp_lds + (16 * y + 8) * kGroups * 4);
+        lds(sz[0], ap + kp_lds + 16 * y * kGroups * 4);
+        lds(sz[1], ap + kp_lds + (16 * y + 8) * kGroups * 4);
         float* sy = s + 4 * y;
         sy[0] = sy[1] = sy[2] = sy[3] = 0.f;
 #pragma unroll
@@ -532,31 +533,31 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         }
       }
       // --- softmax: keys past a row's last (or before its window) have weight 0, whatever they hold
-      bool seen[4 * kHalves];
+      bool seen[4 * kN];
 #pragma unroll
-      for (int e = 0; e < 4 * kHalves; ++e) {
+      for (int e = 0; e < 4 * kN; ++e) {
         seen[e] = true;
         if constexpr (masked.value) {
-          const int key = key0 + kg + 8 * (e / 2), hi = cur.s.L - p.Tq + (rt * 8 + 2 * t + (e & 1)) % p.Tq;
+          const int key = key0 + kg + 8 * (e / 2), hi = cur.s.L - p.Tq + p.row_i[rt * 8 + 2 * t + (e & 1)];
           seen[e] = key <= hi && (p.window < 0 || key >= hi - p.window);
         }
       }
-      float x[4 * kHalves];  // log2 of the weights
+      float x[4 * kN];  // log2 of the weights
       bool raise = false;
 #pragma unroll
-      for (int e = 0; e < 4 * kHalves; ++e) {
+      for (int e = 0; e < 4 * kN; ++e) {
         x[e] = seen[e] ? fmaf(s[e], down[e & 1], -m[e & 1]) : -INFINITY;
         raise |= x[e] > 8.f;
       }
-      uint32_t vsz[2 * kHalves][kGroups];
+      uint32_t vsz[2 * kN][kGroups];
 #pragma unroll
-      for (int y = 0; y < 2 * kHalves; ++y) lds(vsz[y], at + kp_lds + Shape::kParamBytes + 8 * y * kGroups * 4);
+      for (int y = 0; y < 2 * kN; ++y) lds(vsz[y], ap + kp_lds + Shape::kParamBytes + 8 * y * kGroups * 4);
       float top[kGroups];  // the largest scale of this lane's keys
 #pragma unroll
       for (int j = 0; j < kGroups; ++j) {
         top[j] = __uint_as_float(vsz[0][j] << 16);
 #pragma unroll
-        for (int y = 1; y < 2 * kHalves; ++y) top[j] = fmaxf(top[j], __uint_as_float(vsz[y][j] << 16));
+        for (int y = 1; y < 2 * kN; ++y) top[j] = fmaxf(top[j], __uint_as_float(vsz[y][j] << 16));
         raise |= top[j] * unit[j] > 64.f;
       }
       if (__any_sync(0xffffffffu, raise)) {
@@ -564,14 +565,14 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         for (int c = 0; c < 2; ++c) {
           float y = m[c];  // the new max
 #pragma unroll
-          for (int e = c; e < 4 * kHalves; e += 2)
+          for (int e = c; e < 4 * kN; e += 2)
             if (seen[e]) y = fmaxf(y, s[e] * down[c]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
           const float f = ex2(m[c] - y);
           m[c] = y;
 #pragma unroll
-          for (int e = c; e < 4 * kHalves; e += 2)
+          for (int e = c; e < 4 * kN; e += 2)
             if (seen[e]) x[e] = fmaf(s[e], down[c], -y);
           l[c] *= f;
 #pragma unroll
@@ -586,8 +587,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
           for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
           if (y * unit[j] > 64.f) {  // the unit becomes the largest scale's power of two
             const int e = static_cast<int>(__float_as_uint(y) >> 23);  // its exponent field
-            const float to = __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 1), 254)) << 23);
-            const float f = to / unit[j];
+            const float to = __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 1), 253)) << 23);
+            const float f = to * kvq_inverse(unit[j]);
             unit[j] = to;
 #pragma unroll
             for (int i = j * (kGroup / 16); i < (j + 1) * (kGroup / 16); ++i)
@@ -596,13 +597,13 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4 * kHalves; ++e) {
+      for (int e = 0; e < 4 * kN; ++e) {
         x[e] = ex2(x[e]);
         l[e & 1] += x[e];
       }
       // --- values
 #pragma unroll
-      for (int y = 0; y < kHalves; ++y) {
+      for (int y = 0; y < kN; ++y) {
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
           uint32_t b[2];  // the weights of keys kg (+ 8) and columns 2 t, 2 t + 1, then transposed
@@ -665,9 +666,12 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       fetch(stage == 0 ? kStages - 1 : stage - 1);
       const uint32_t at = ring + stage * Shape::kStageBytes;
       if (key0 + kTile - 1 <= cur.s.L - p.Tq && (p.window < 0 || key0 >= cur.s.L - 1 - p.window))
-        tile(at, key0, std::false_type());  // every row sees every key
-      else
-        tile(at, key0, std::true_type());
+        tile(at, at + 2 * Shape::kCodeBytes, key0, std::false_type(), std::integral_constant<int, kHalves>());
+      else  // some row does not see some key: rare in long caches, and kept small
+#pragma unroll 1
+        for (int y = 0; y < kHalves; ++y)
+          tile(at + 16 * y * kRowBytes, at + 2 * Shape::kCodeBytes + 16 * y * kGroups * 4, key0 + 16 * y,
+               std::true_type(), std::integral_constant<int, 1>());
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
@@ -683,7 +687,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
     }
     float worth[kGroups];  // 2^24 of the codes, and what a weight's unit is
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) worth[j] = 0x1p24f / unit[j];
+    for (int j = 0; j < kGroups; ++j) worth[j] = 0x1p24f * kvq_inverse(unit[j]);
     constexpr float kSecond = kBits == 4 ? 0.0625f : 1.f;  // rows g + 8 of a tile: second (fourth) nibbles
     const bool whole = cur.tile == 0 && piece_end == unit_end;
     const int slot = lin == first ? 0 : 1;
@@ -693,8 +697,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
     for (int c = 0; c < 2; ++c) {
       const int r = rt * 8 + 2 * t + c;
       if (r >= R) continue;
-      const int i = r % p.Tq, h = cur.hk * G + r / p.Tq;
-      const float inv = l[c] == 0.f ? 0.f : 1.f / l[c];  // (a row that sees no key: 0)
+      const int i = p.row_i[r], h = cur.hk * G + p.row_g[r];
+      const float inv = kvq_factor(l[c]);
       const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128;
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
@@ -711,64 +715,79 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       if (!whole)
         *reinterpret_cast<float2*>(piece_ml(slot, warp) + (2 * t + c) * 2) = make_float2(m[c], l[c]);
       else if (ATTN_IN_RANGE(lse_i, 1, n_q / 128, kSiteKvqDecLse, &g_kvq_error))
-        p.lse[lse_i] = l[c] == 0.f ? -INFINITY : (m[c] + log2f(l[c])) * 0.69314718055994531f;
+        p.lse[lse_i] = kvq_lse(m[c], l[c]);
     }
     if (!whole && lane == 0 && rt == 0)
-      sh_piece[slot][slice] = KvqPiece{cur.b * p.Hkv + cur.hk, cur.tile == 0, unit_end};
+      sh_piece[2 * slice + slot] = KvqPiece{cur.b * p.Hkv + cur.hk, cur.tile == 0, unit_end};
     lin = piece_end;
     cur.tile = 0;
     if (lin < last) kvq_next_unit<kTile>(p, cur);
+  }
+  // Sequences without keys: o = 0, lse = -inf, shared out over the CTAs.
+  for (int b = __any_sync(0xffffffffu, empty) ? blockIdx.x : p.B; b < p.B; b += gridDim.x) {
+    if (kvq_seq<kTile>(p, b).tiles > 0) continue;
+    uint4* o4 = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(b) * p.Tq * p.H * 128);
+    for (int i = tid; i < p.Tq * p.H * 16; i += kKvqThreads) o4[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < p.Tq * p.H; i += kKvqThreads) p.lse[static_cast<size_t>(b) * p.Tq * p.H + i] = -INFINITY;
   }
   cp_async_wait<0>();
   __syncthreads();
 
   // --- the CTA's pieces of one unit, joined by their maxima: a chain begins with a stretch's last piece, or with its
-  // first where the unit begins there (or the CTA does), and goes on through the first pieces of the stretches after it.
+  // first where the unit begins there (or the CTA does), and goes on through the first pieces of the stretches after
+  // it. Lane i looks at piece i; a chain's pieces are then the lanes from its head up to the next head.
+  static_assert(2 * kKvqWarps <= 32, "a lane per piece");
   const int cta_end = start_of(slices);
-  for (int i = 0, n = 0; i < 2 * slices; ++i) {
-    const int s0 = i / 2, slot0 = i % 2;
-    const KvqPiece head = sh_piece[slot0][s0];
-    if (head.unit < 0 || !(slot0 || head.begins || s0 == 0)) continue;
-    int s1 = s0 + 1;  // the chain is head, then the first pieces of stretches s0 + 1 .. s1 - 1
-    while (s1 < slices && sh_piece[0][s1].unit == head.unit) ++s1;
-    const bool ends = head.end <= cta_end, whole = head.begins && ends;
-    const int cta_slot = i == 0 ? 0 : 1;
-    const int b = head.unit / p.Hkv, hk = head.unit % p.Hkv;
+  KvqPiece pc = {-1, 0, 0};
+  if (lane < 2 * slices) pc = sh_piece[lane];
+  const unsigned have = __ballot_sync(0xffffffffu, pc.unit >= 0);
+  unsigned heads = __ballot_sync(0xffffffffu, pc.unit >= 0 && ((lane & 1) || pc.begins || lane == 0));
+  for (int n = 0; heads; ++n) {
+    const int i0 = __ffs(heads) - 1;
+    heads &= heads - 1;
+    const unsigned chain = have & (0xffffffffu << i0) & (heads ? (1u << (__ffs(heads) - 1)) - 1u : 0xffffffffu);
+    const int unit = __shfl_sync(0xffffffffu, pc.unit, i0), end = __shfl_sync(0xffffffffu, pc.end, i0);
+    const bool begins = __shfl_sync(0xffffffffu, pc.begins, i0), ends = end <= cta_end;
+    const int b = unit / p.Hkv, hk = unit % p.Hkv;
     for (int r = (warp + 64 * kKvqWarps - n * R) % kKvqWarps; r < R; r += kKvqWarps) {  // rows of all chains in turn
-      auto at = [&](int s) { return s * n_rt + r / 8; };                 // the warp of stretch s that had row r
-      float M = piece_ml(slot0, at(s0))[(r % 8) * 2];
-      for (int s = s0 + 1; s < s1; ++s) M = fmaxf(M, piece_ml(0, at(s))[(r % 8) * 2]);
-      float L = 0.f;
+      // piece `lane` of row r: its warp is that of the stretch and the row's tile
+      float2 ml = make_float2(kNone, 0.f);
+      if (chain >> lane & 1)
+        ml = *reinterpret_cast<const float2*>(piece_ml(lane & 1, (lane / 2) * n_rt + r / 8) + (r % 8) * 2);
+      float M = ml.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float f = ex2(ml.x - M);
+      float L = ml.y * f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
       float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = s0; s < s1; ++s) {
-        const int slot = s == s0 ? slot0 : 0;
-        const float2 ml = *reinterpret_cast<const float2*>(piece_ml(slot, at(s)) + (r % 8) * 2);
-        const float4 x = *reinterpret_cast<const float4*>(piece_o(slot, at(s)) + (r % 8) * 128 + lane * 4);
-        const float f = ex2(ml.x - M);
-        L = fmaf(ml.y, f, L);
-        o4.x = fmaf(x.x, f, o4.x), o4.y = fmaf(x.y, f, o4.y), o4.z = fmaf(x.z, f, o4.z), o4.w = fmaf(x.w, f, o4.w);
+      for (unsigned c = chain; c; c &= c - 1) {
+        const int i = __ffs(c) - 1;
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float4 x = *reinterpret_cast<const float4*>(piece_o(i & 1, (i / 2) * n_rt + r / 8) + (r % 8) * 128 + lane * 4);
+        o4.x = fmaf(x.x, fi, o4.x), o4.y = fmaf(x.y, fi, o4.y), o4.z = fmaf(x.z, fi, o4.z), o4.w = fmaf(x.w, fi, o4.w);
       }
-      if (whole) {
-        const int q = r % p.Tq, h = hk * G + r / p.Tq;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+      if (begins && ends) {
+        const int q = p.row_i[r], h = hk * G + p.row_g[r];
+        const float inv = kvq_factor(L);
         const size_t off = ((static_cast<size_t>(b) * p.Tq + q) * p.H + h) * 128 + lane * 4;
         if (ATTN_IN_RANGE(off, 4, n_q, kSiteKvqDecO, &g_kvq_error))
           *reinterpret_cast<uint2*>(p.o + off) =
               make_uint2(sm100::pack_bf16x2(o4.x * inv, o4.y * inv), sm100::pack_bf16x2(o4.z * inv, o4.w * inv));
         const size_t lse_i = (static_cast<size_t>(b) * p.H + h) * p.Tq + q;
-        if (lane == 0 && ATTN_IN_RANGE(lse_i, 1, n_q / 128, kSiteKvqDecLse, &g_kvq_error))
-          p.lse[lse_i] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        if (lane == 0 && ATTN_IN_RANGE(lse_i, 1, n_q / 128, kSiteKvqDecLse, &g_kvq_error)) p.lse[lse_i] = kvq_lse(M, L);
       } else {
-        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + cta_slot) * R + r;
+        const int slot = i0 == 0 ? 0 : 1;
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + slot) * R + r;
         if (ATTN_IN_RANGE(part, 1, static_cast<size_t>(gridDim.x) * 2 * R, kSiteKvqDecPart, &g_kvq_error)) {
           *reinterpret_cast<float4*>(p.part_o + part * 128 + lane * 4) = o4;
           if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(M, L);
         }
+        if (r == 0 && lane == 0 && begins)  // it begins here and goes on past this CTA
+          p.spans[blockIdx.x] = KvqSpan{unit, (end - 1) / (share * slices), slot, 0};
       }
-      if (r == 0 && lane == 0 && head.begins && !ends)  // it begins here and goes on past this CTA
-        p.spans[blockIdx.x] = KvqSpan{head.unit, (head.end - 1) / (share * slices), cta_slot, 0};
     }
-    ++n;
   }
 }
 
@@ -815,8 +834,8 @@ __global__ void __launch_bounds__(256) kvq_decode_merge_kernel(const KvqDecodePa
     o4.x += v.x, o4.y += v.y, o4.z += v.z, o4.w += v.w;
     l += sh_sum[w];
   }
-  const int b = span.unit / p.Hkv, hk = span.unit % p.Hkv, i = r % p.Tq, h = hk * (p.H / p.Hkv) + r / p.Tq;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int b = span.unit / p.Hkv, hk = span.unit % p.Hkv, i = p.row_i[r], h = hk * (p.H / p.Hkv) + p.row_g[r];
+  const float inv = kvq_factor(l);
   const size_t n_out = static_cast<size_t>(p.B) * p.Tq * p.H;
   (void)n_out;
   const size_t off = (static_cast<size_t>(b) * p.Tq + i) * p.H + h;
@@ -825,7 +844,7 @@ __global__ void __launch_bounds__(256) kvq_decode_merge_kernel(const KvqDecodePa
         make_uint2(sm100::pack_bf16x2(o4.x * inv, o4.y * inv), sm100::pack_bf16x2(o4.z * inv, o4.w * inv));
   const size_t lse_i = (static_cast<size_t>(b) * p.H + h) * p.Tq + i;
   if (lane == 0 && ATTN_IN_RANGE(lse_i, 1, n_out, kSiteKvqDecLse, &g_kvq_error))
-    p.lse[lse_i] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+    p.lse[lse_i] = kvq_lse(M, l);
 }
 
 }  // namespace attn
