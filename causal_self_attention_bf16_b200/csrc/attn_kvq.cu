@@ -44,6 +44,12 @@ struct CopyParams {
   int B, T, Hkv, Tk;
 };
 
+// A kernel launched by launch_early: wait for the grid before it, and let the next one start up.
+__device__ __forceinline__ void begin_early() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Row r of [B, T, H_kv] (token i of sequence b, head h): its cache row, or -1 where the token has no position.
 __device__ __forceinline__ long long cache_row(const CopyParams& p, int r) {
   const int h = r % p.Hkv, bi = r / p.Hkv, b = bi / p.T, i = bi % p.T;
@@ -102,6 +108,7 @@ __device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t* sz) {
 
 template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(const CopyParams p) {
+  begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
   const int c = threadIdx.x % kChunks;
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
@@ -133,6 +140,7 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(const CopyParam
 
 template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(const CopyParams p) {
+  begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
   const int c = threadIdx.x % kChunks;
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
@@ -237,15 +245,32 @@ void with_format(int bits, int group, F&& f) {
   else by_group(integral_constant<int, 8>());
 }
 
+// Launches a kernel that may start while the one before it in the stream still runs: each of this file's kernels waits
+// for that one's end (griddepcontrol.wait) before it touches memory, so only its start-up overlaps.
+template <typename P>
+cudaError_t launch_early(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 attn_status launch_copy(bool write, const CopyParams& p, int bits, int group, void* stream) {
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
   const unsigned grid = static_cast<unsigned>((rows + kCopyThreads / kChunks - 1) / (kCopyThreads / kChunks));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
   with_format(bits, group, [&](auto b, auto g) {
-    if (write) kvq_write_kernel<b.value, g.value><<<grid, kCopyThreads, 0, s>>>(p);
-    else kvq_read_kernel<b.value, g.value><<<grid, kCopyThreads, 0, s>>>(p);
+    e = launch_early(write ? kvq_write_kernel<b.value, g.value> : kvq_read_kernel<b.value, g.value>, dim3(grid),
+                     kCopyThreads, 0, s, p);
   });
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, write ? "kvq_write_kernel launch" : "kvq_read_kernel launch");
   return ATTN_OK;
 }
@@ -287,8 +312,7 @@ cudaError_t launch_split(const attn::KvqDecodeParams& p, unsigned ctas, cudaStre
   static_assert(kSmem + 1024 <= 227 * 1024, "one CTA per SM");
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, attn::kKvqThreads, kSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(kernel, dim3(ctas), attn::kKvqThreads, kSmem, s, p);
 }
 
 }  // namespace
@@ -409,18 +433,16 @@ attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_pa
   });
   if (e != cudaSuccess) return cuda_fail(e, "kvq_decode_split_kernel launch");
   if (ctas > 1) {
-    // Launched while the split kernel runs (its blocks wait for that grid's end), so that its start costs nothing.
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, R);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, attn::kvq_decode_merge_kernel, p)) != cudaSuccess)
-      return cuda_fail(e, "kvq_decode_merge_kernel launch");
+    // A unit spans about ctas / (B * H_kv) CTAs: with many pieces to a unit a block takes one row, with few up to 8.
+    if (R == 1 || static_cast<long long>(B) * H_kv * 8 < ctas)
+      e = launch_early(attn::kvq_decode_merge_kernel<1>, dim3(ctas, R), 256, 0, s, p);
+    else if (R == 2)
+      e = launch_early(attn::kvq_decode_merge_kernel<2>, dim3(ctas), 256, 0, s, p);
+    else if (R <= 4)
+      e = launch_early(attn::kvq_decode_merge_kernel<4>, dim3(ctas), 256, 0, s, p);
+    else
+      e = launch_early(attn::kvq_decode_merge_kernel<8>, dim3(ctas, (R + 7) / 8), 256, 0, s, p);
+    if (e != cudaSuccess) return cuda_fail(e, "kvq_decode_merge_kernel launch");
   }
   return ATTN_OK;
 }

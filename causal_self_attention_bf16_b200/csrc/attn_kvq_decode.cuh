@@ -25,11 +25,12 @@
 //   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 8 (then p <= 2^8
 //   and the sums stay far from overflow): one vote a tile in place of the reduction and the rescaling.
 //
-// Work split. A unit is one (sequence, key/value head); its visible keys, tiles of 16. All units' tiles in a row are
-// dealt to the warps in equal stretches, found on the device from the lengths, so that every warp reads the same number
-// of bytes however ragged the batch, through a ring of tiles in shared memory that it fills for itself (cp.async; no
-// barrier in the loop). A unit that begins and ends in one warp's stretch is finished there; the pieces of one that
-// spans warps are joined by the CTA at its end, and the CTAs' pieces by kvq_decode_merge_kernel.
+// Work split. A unit is one (sequence, key/value head); its visible keys, tiles of 32 (8 bits: 16). All units' tiles in a
+// row, with a place more for each unit's own cost, are dealt to the warps in equal stretches, found on the device from
+// the lengths, so that every warp has the same work however ragged the batch, through a ring of tiles in shared memory
+// that it fills for itself (cp.async; no barrier in the loop). A unit that begins and ends in one warp's stretch is
+// finished there; the pieces of one that spans warps are joined by the CTA at its end, and the CTAs' pieces by
+// kvq_decode_merge_kernel.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -49,6 +50,10 @@ constexpr int kKvqWarps = 12;     // warps per CTA (divides by 1, 2, 3 and 4 row
 constexpr int kKvqThreads = kKvqWarps * 32;
 constexpr int kKvqCtas = 148;     // CTAs of the split kernel, at most: one per SM of a 148-SM part
 
+// Places of a unit in the row beside its tiles: its queries, its first maximum and its result take a warp about as long
+// as two tiles do (one or none measured 3 and 20 % slower on decode_d20, whose batch holds short sequences).
+constexpr int kKvqUnitCost = 2;
+
 enum : uint32_t {
   kSiteKvqDecQ = 0xa4, kSiteKvqDecCodes = 0xa5, kSiteKvqDecParams = 0xa6, kSiteKvqDecO = 0xa7, kSiteKvqDecLse = 0xa8,
   kSiteKvqDecPart = 0xa9
@@ -66,7 +71,7 @@ struct KvqSpan {
 struct KvqPiece {
   int unit;    // b * H_kv + hk, or -1: none
   int begins;  // the unit's first tile is the piece's
-  int end;     // the unit's end in the row of all tiles
+  int end;     // the unit's end in the row of all places
 };
 
 struct KvqDecodeParams {
@@ -274,52 +279,71 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   __shared__ KvqPiece sh_piece[2 * kKvqWarps];  // stretch i's slots at 2 i, 2 i + 1
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int R = p.R, G = p.H / p.Hkv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");               // (this grid may be launched before the one it follows ends)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge kernel waits for this grid's end)
+  const int n_rt = (R + 7) / 8;
+  const int slices = kKvqWarps / n_rt;  // stretches per CTA, each for the n_rt warps of its row tiles
+  const int rt = warp % n_rt, slice = warp / n_rt;
+  if (rt == 0 && lane < 2) sh_piece[2 * slice + lane].unit = -1;  // (this warp's to write; read after the barrier)
   if (tid == 0) p.spans[blockIdx.x].unit = -1;
 
-  // All units' tiles, then where this warp's stretch of them begins: every warp looks for itself, 32 sequences at a
-  // time.
+  // Every warp looks for itself where its stretch of the row of all places begins and ends, 32 sequences at a time. A
+  // sequence without tiles has no places; otherwise each of its units has kKvqUnitCost places, then its tiles'.
+  auto places = [&](int b) {
+    const int n = b < p.B ? kvq_seq<kTile>(p, b).tiles : 0;
+    return n ? (n + kKvqUnitCost) * p.Hkv : 0;
+  };
   int total = 0;
   bool empty = false;  // whether there are sequences without keys
   for (int b = lane; b < p.B; b += 32) {
-    const int n = kvq_seq<kTile>(p, b).tiles;
+    const int n = places(b);
     total += n;
     empty |= n == 0;
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  total *= p.Hkv;
-  const int n_rt = (R + 7) / 8;
-  const int slices = kKvqWarps / n_rt;  // stretches per CTA, each for the n_rt warps of its row tiles
-  const int rt = warp % n_rt, slice = warp / n_rt;
-  if (rt == 0 && lane < 2) sh_piece[2 * slice + lane].unit = -1;  // (this warp's to write; read after the barrier)
   const int share = (total + static_cast<int>(gridDim.x) * slices - 1) / (static_cast<int>(gridDim.x) * slices);
-  // Stretch i of this CTA is tiles [start_of(i), start_of(i + 1)).
+  // Stretch i of this CTA is places [start_of(i), start_of(i + 1)).
   auto start_of = [&](int i) {
     return static_cast<int>(min(static_cast<long long>(total), (static_cast<long long>(blockIdx.x) * slices + i) * share));
   };
   const int first = start_of(slice), last = start_of(slice + 1);
   KvqCursor cur = {};  // the unit being computed
+  int unit_end = 0;    // its end in the row of all places
+  int left = 0;        // tiles of the stretch still to be fetched
   if (first < last) {
-    for (int b0 = 0, before = 0;; b0 += 32) {
-      const int b = b0 + lane, n = b < p.B ? kvq_seq<kTile>(p, b).tiles * p.Hkv : 0;
+    // The stretch's tiles are those whose places it has; its first unit may have begun before it.
+    for (int b0 = 0, before = 0; b0 < p.B; b0 += 32) {
+      const int n = places(b0 + lane);
       int incl = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += y;
       }
+      // places of this lane's sequence within the stretch, less its units' own among them
+      const int lo = max(first - (before + incl - n), 0), hi = min(last - (before + incl - n), n);
+      int mine = 0;
+      if (lo < hi) {
+        const int each = n / p.Hkv;
+        const int u0 = lo / each, u1 = hi / each;
+        mine = (u1 - u0) * (each - kKvqUnitCost) + max(hi - u1 * each - kKvqUnitCost, 0) - max(lo - u0 * each - kKvqUnitCost, 0);
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+      left += mine;
       const unsigned past = __ballot_sync(0xffffffffu, before + incl > first);
-      if (past) {  // (some sequence ends past it: first < total)
-        const int l = __ffs(past) - 1;
+      if (past && unit_end == 0) {  // the stretch begins in the first of these sequences
+        const int l = __ffs(past) - 1, start = before + __shfl_sync(0xffffffffu, incl - n, l);
         cur.b = b0 + l;
         cur.s = kvq_seq<kTile>(p, cur.b);
-        const int off = first - (before + __shfl_sync(0xffffffffu, incl - n, l));
-        cur.hk = off / cur.s.tiles;
-        cur.tile = off - cur.hk * cur.s.tiles;
-        break;
+        const int each = cur.s.tiles + kKvqUnitCost;
+        cur.hk = (first - start) / each;
+        unit_end = start + (cur.hk + 1) * each;
+        cur.tile = max(first - (unit_end - each) - kKvqUnitCost, 0);
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
+      if (before >= last) break;
     }
   }
 
@@ -337,7 +361,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   const size_t n_rows = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_rows;
   KvqCursor pre = cur;  // the next tile this warp fetches
-  int pre_lin = first;
+  int pre_left = left;
   // its first row's codes at this lane's chunk, and its params (the lower half warp fetches the keys', the upper the
   // values')
   const uint8_t *k_from, *v_from, *p_from;
@@ -350,7 +374,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
              (pre_row + p_row) * (kGroups * 4);
   };
   auto fetch = [&](int stage) {  // copies (or nothing) and one commit
-    if (pre_lin < last) {
+    if (pre_left > 0) {
       if (pre.tile == pre.s.tiles) {
         pre.tile = 0;
         kvq_next_unit<kTile>(p, pre);
@@ -383,7 +407,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
                                 in ? p_from + i * 64 * kGroups : reinterpret_cast<const uint8_t*>(p.k_params), in);
         }
       }
-      ++pre_lin;
+      --pre_left;
       ++pre.tile;
       pre_row += kTile;
       k_from += kTile * kRowBytes;
@@ -415,10 +439,11 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   const size_t n_q = static_cast<size_t>(p.B) * p.Tq * p.H * 128;
   (void)n_q;
 
-  int stage = 0, lin = first;  // lin: first tile of the current piece
-  while (lin < last) {
-    // --- one piece: tiles [lin, piece_end) of unit (cur.b, cur.hk), from its tile cur.tile on
-    const int unit_end = lin - cur.tile + cur.s.tiles, piece_end = min(last, unit_end);
+  int stage = 0;
+  for (int slot = 0; left > 0; slot = 1) {
+    // --- one piece: n_tiles tiles of unit (cur.b, cur.hk), from its tile cur.tile on
+    const int n_tiles = min(left, cur.s.tiles - cur.tile);
+    const bool whole = n_tiles == cur.s.tiles;
     // The unit's queries as B fragments: column g is row rt * 8 + g; the lane holds its dims that meet the words of a
     // key row that it reads, paired as the codes are, in units of 2^-up (4 bits: second and fourth nibbles 2^(4 - up),
     // as their codes are 2^4 larger).
@@ -430,6 +455,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128;
       const bool live = row < R && ATTN_IN_RANGE(off, 128, n_q, kSiteKvqDecQ, &g_kvq_error);
       uint4 u[4];
+      float qs[kGroups][4];
       uint32_t top = 0;  // the largest exponent, bf16 bits 7-14 of a half
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -445,17 +471,14 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       // 2^up brings exponent `top` to 2^14 (an infinity or NaN stays one); 2^up and 2^-up are normal numbers
       const int up = min(14 + 127 - static_cast<int>(top >> 7), 126);
       const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-      float part = 0.f;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const uint32_t w[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
         uint32_t f[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float a = __uint_as_float(w[y] << 16) * mul, b = __uint_as_float(w[y] & 0xffff0000u) * mul;
-          f[y] = pack_f16x2(a, kBits == 4 ? b * 0.0625f : b);
-          part += a + b;
-        }
+        for (int y = 0; y < 4; ++y)
+          f[y] = pack_f16x2(__uint_as_float(w[y] << 16) * mul,
+                            __uint_as_float(w[y] & 0xffff0000u) * (kBits == 4 ? mul * 0.0625f : mul));
         if constexpr (kBits == 4) {  // dims (0,4) (1,5) (2,6) (3,7) of a word's eight
           qb[4 * x] = __byte_perm(f[0], f[2], 0x5410);
           qb[4 * x + 1] = __byte_perm(f[0], f[2], 0x7632);
@@ -465,14 +488,13 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
           for (int y = 0; y < 4; ++y) qb[4 * x + y] = f[y];
         }
-        if ((x + 1) % (kGroup / 32) == 0) {
-          const int j = x / (kGroup / 32);
-          part += __shfl_xor_sync(0xffffffffu, part, 1);
-          part += __shfl_xor_sync(0xffffffffu, part, 2);
-          qsum[j][0] = __shfl_sync(0xffffffffu, part, 8 * t) * 0x1p-24f;
-          qsum[j][1] = __shfl_sync(0xffffffffu, part, 8 * t + 4) * 0x1p-24f;
-          part = 0.f;
-        }
+        // the sums of q over a group's dims: products with 2^-24 everywhere (2^-20 for the numbers that are 2^4 smaller)
+        constexpr uint32_t kOne = 0x00010001u, kSecond = kBits == 4 ? 0x00100010u : kOne;
+        const int j = x / (kGroup / 32);
+        if (x % (kGroup / 32) == 0) mma_16x8x16_first(qs[j], kOne, kOne, kSecond, kSecond, qb[4 * x], qb[4 * x + 1]);
+        else mma_16x8x16(qs[j], kOne, kOne, kSecond, kSecond, qb[4 * x], qb[4 * x + 1]);
+        mma_16x8x16(qs[j], kOne, kOne, kSecond, kSecond, qb[4 * x + 2], qb[4 * x + 3]);
+        qsum[j][0] = qs[j][0], qsum[j][1] = qs[j][1];
       }
       const float back = (p.scale_log2 * 0x1p24f) * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
       down[0] = __shfl_sync(0xffffffffu, back, 8 * t);
@@ -660,7 +682,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
     };
 
     int key0 = cur.s.start + cur.tile * kTile;
-    for (int n = piece_end - lin; n > 0; --n, key0 += kTile) {
+    for (int n = n_tiles; n > 0; --n, key0 += kTile) {
       cp_async_wait<kStages - 2>();
       __syncwarp();  // this tile is in, and every lane has read the one before it
       fetch(stage == 0 ? kStages - 1 : stage - 1);
@@ -689,8 +711,6 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) worth[j] = 0x1p24f * kvq_inverse(unit[j]);
     constexpr float kSecond = kBits == 4 ? 0.0625f : 1.f;  // rows g + 8 of a tile: second (fourth) nibbles
-    const bool whole = cur.tile == 0 && piece_end == unit_end;
-    const int slot = lin == first ? 0 : 1;
     if (!whole && slot) __syncwarp();  // (every lane has read the last tile, which the piece overwrites)
     float* to_o = piece_o(slot, warp);
 #pragma unroll
@@ -719,9 +739,12 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
     }
     if (!whole && lane == 0 && rt == 0)
       sh_piece[2 * slice + slot] = KvqPiece{cur.b * p.Hkv + cur.hk, cur.tile == 0, unit_end};
-    lin = piece_end;
+    left -= n_tiles;
     cur.tile = 0;
-    if (lin < last) kvq_next_unit<kTile>(p, cur);
+    if (left > 0) {
+      kvq_next_unit<kTile>(p, cur);
+      unit_end += cur.s.tiles + kKvqUnitCost;
+    }
   }
   // Sequences without keys: o = 0, lse = -inf, shared out over the CTAs.
   for (int b = __any_sync(0xffffffffu, empty) ? blockIdx.x : p.B; b < p.B; b += gridDim.x) {
@@ -793,47 +816,76 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 
 // ------------------------------------------------------------------------------------------------ merge kernel
 
-// Block (x, r): row r of the unit that begins in the split kernel's CTA x and goes on past it, if there is one:
-// O = sum_s O_s 2^(m_s - M) / sum_s l_s 2^(m_s - M) over its pieces, M = max_s m_s. The pieces are shared by the
-// block's warps, a lane taking four dims, and the warps' sums are added in order.
+// Block (x, y): rows kRows y .. kRows (y + 1) - 1 of the unit that begins in the split kernel's CTA x and goes on past it,
+// if there is one: O = sum_s O_s 2^(m_s - M) / sum_s l_s 2^(m_s - M) over its pieces, M = max_s m_s. The block's 8 warps
+// share the rows and, where there are fewer rows, each row's pieces; a lane takes four dims. A running maximum as in the
+// split kernel, so that a piece is read once, with its maximum and sum.
+template <int kRows>
 __global__ void __launch_bounds__(256) kvq_decode_merge_kernel(const KvqDecodeParams p) {
-  __shared__ float sh_max[8], sh_sum[8];
+  constexpr int kSlices = 8 / kRows;  // warps that share a row's pieces
+  __shared__ float2 sh_ml[8];
   __shared__ float4 sh_o[8][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's results
-  const int x = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32, R = p.R;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int x = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32, R = p.R;
   const KvqSpan span = p.spans[x];
   if (span.unit < 0) return;
   const int n = span.last_cta - x + 1;  // pieces: this CTA's slot, then the first slot of each CTA after it
   if (!ATTN_IN_RANGE(span.last_cta, 1, gridDim.x, kSiteKvqDecPart, &g_kvq_error)) return;
-  auto part = [&](int s) { return (static_cast<size_t>(x + s) * 2 + (s == 0 ? span.slot : 0)) * R + r; };
-  float M = -INFINITY;
-  for (int s = tid; s < n; s += 256) M = fmaxf(M, p.part_ml[part(s) * 2]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) sh_max[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, sh_max[w]);
-  float l = 0.f;
+  const int r = blockIdx.y * kRows + warp / kSlices;
+  float M = -3e38f, l = 0.f;
   float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = warp; s < n; s += 8) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + part(s) * 2);
-    const float4 v = reinterpret_cast<const float4*>(p.part_o + part(s) * 128)[lane];
-    const float f = ex2(ml.x - M);
-    l = fmaf(ml.y, f, l);
-    o4.x = fmaf(v.x, f, o4.x), o4.y = fmaf(v.y, f, o4.y), o4.z = fmaf(v.z, f, o4.z), o4.w = fmaf(v.w, f, o4.w);
-  }
-  sh_o[warp][lane] = o4;
-  if (lane == 0) sh_sum[warp] = l;
-  __syncthreads();
-  if (warp) return;
+  if (r < R) {
+    constexpr int kAtOnce = 4;
+    for (int s0 = warp % kSlices; s0 < n; s0 += kAtOnce * kSlices) {
+      float2 ml[kAtOnce];
+      float4 v[kAtOnce];
+      float top = M;
 #pragma unroll
-  for (int w = 1; w < 8; ++w) {
-    const float4 v = sh_o[w][lane];
-    o4.x += v.x, o4.y += v.y, o4.z += v.z, o4.w += v.w;
-    l += sh_sum[w];
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int s = s0 + u * kSlices;
+        ml[u] = make_float2(-INFINITY, 0.f), v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < n) {
+          const size_t part = (static_cast<size_t>(x + s) * 2 + (s == 0 ? span.slot : 0)) * R + r;
+          ml[u] = *reinterpret_cast<const float2*>(p.part_ml + part * 2);
+          v[u] = reinterpret_cast<const float4*>(p.part_o + part * 128)[lane];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, ml[u].x);
+      const float down = ex2(M - top);
+      M = top;
+      l *= down, o4.x *= down, o4.y *= down, o4.z *= down, o4.w *= down;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const float f = ex2(ml[u].x - M);
+        l = fmaf(ml[u].y, f, l);
+        o4.x = fmaf(v[u].x, f, o4.x), o4.y = fmaf(v[u].y, f, o4.y);
+        o4.z = fmaf(v[u].z, f, o4.z), o4.w = fmaf(v[u].w, f, o4.w);
+      }
+    }
   }
+  if constexpr (kSlices > 1) {  // the row's first warp adds up the others' sums
+    sh_o[warp][lane] = o4;
+    if (lane == 0) sh_ml[warp] = make_float2(M, l);
+    __syncthreads();
+    if (warp % kSlices) return;
+    float top = M;
+#pragma unroll
+    for (int w = 1; w < kSlices; ++w) top = fmaxf(top, sh_ml[warp + w].x);
+    const float down = ex2(M - top);
+    M = top;
+    l *= down, o4.x *= down, o4.y *= down, o4.z *= down, o4.w *= down;
+#pragma unroll
+    for (int w = 1; w < kSlices; ++w) {
+      const float2 ml = sh_ml[warp + w];
+      const float4 v = sh_o[warp + w][lane];
+      const float f = ex2(ml.x - M);
+      l = fmaf(ml.y, f, l);
+      o4.x = fmaf(v.x, f, o4.x), o4.y = fmaf(v.y, f, o4.y), o4.z = fmaf(v.z, f, o4.z), o4.w = fmaf(v.w, f, o4.w);
+    }
+  }
+  if (r >= R) return;
   const int b = span.unit / p.Hkv, hk = span.unit % p.Hkv, i = p.row_i[r], h = hk * (p.H / p.Hkv) + p.row_g[r];
   const float inv = kvq_factor(l);
   const size_t n_out = static_cast<size_t>(p.B) * p.Tq * p.H;
@@ -843,8 +895,7 @@ __global__ void __launch_bounds__(256) kvq_decode_merge_kernel(const KvqDecodePa
     reinterpret_cast<uint2*>(p.o + off * 128)[lane] =
         make_uint2(sm100::pack_bf16x2(o4.x * inv, o4.y * inv), sm100::pack_bf16x2(o4.z * inv, o4.w * inv));
   const size_t lse_i = (static_cast<size_t>(b) * p.H + h) * p.Tq + i;
-  if (lane == 0 && ATTN_IN_RANGE(lse_i, 1, n_out, kSiteKvqDecLse, &g_kvq_error))
-    p.lse[lse_i] = kvq_lse(M, l);
+  if (lane == 0 && ATTN_IN_RANGE(lse_i, 1, n_out, kSiteKvqDecLse, &g_kvq_error)) p.lse[lse_i] = kvq_lse(M, l);
 }
 
 }  // namespace attn
