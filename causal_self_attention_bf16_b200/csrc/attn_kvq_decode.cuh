@@ -245,22 +245,26 @@ __device__ __forceinline__ KvqSeq kvq_seq(const KvqDecodeParams& p, int b) {
   return s;
 }
 
-// A place in the row of all units' tiles.
+// A tile of a unit, and the unit's end in the row of all places.
 struct KvqCursor {
-  int b, hk, tile;
+  int b, hk, tile, end;
   KvqSeq s;
 };
+// The first tile of the next unit; the end of all places where there is none.
 template <int kTile>
 __device__ __forceinline__ void kvq_next_unit(const KvqDecodeParams& p, KvqCursor& c) {
-  if (++c.hk < p.Hkv) return;
-  c.hk = 0;
-  do {
-    if (++c.b >= p.B) {
-      c.s.tiles = 0x7fffffff;  // (past the last unit: never asked for)
-      return;
-    }
-    c.s = kvq_seq<kTile>(p, c.b);
-  } while (c.s.tiles == 0);
+  c.tile = 0;
+  if (++c.hk == p.Hkv) {
+    c.hk = 0;
+    do {
+      if (++c.b >= p.B) {
+        c.end = 0x7fffffff;
+        return;
+      }
+      c.s = kvq_seq<kTile>(p, c.b);
+    } while (c.s.tiles == 0);
+  }
+  c.end += kKvqUnitCost + c.s.tiles;
 }
 
 // ------------------------------------------------------------------------------------------------ split kernel
@@ -287,8 +291,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   if (rt == 0 && lane < 2) sh_piece[2 * slice + lane].unit = -1;  // (this warp's to write; read after the barrier)
   if (tid == 0) p.spans[blockIdx.x].unit = -1;
 
-  // Every warp looks for itself where its stretch of the row of all places begins and ends, 32 sequences at a time. A
-  // sequence without tiles has no places; otherwise each of its units has kKvqUnitCost places, then its tiles'.
+  // Every warp looks for itself where its stretch of the row of all places begins, 32 sequences at a time. A sequence
+  // without tiles has no places; otherwise each of its units has kKvqUnitCost places, then its tiles'.
   auto places = [&](int b) {
     const int n = b < p.B ? kvq_seq<kTile>(p, b).tiles : 0;
     return n ? (n + kKvqUnitCost) * p.Hkv : 0;
@@ -302,18 +306,18 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  const int share = (total + static_cast<int>(gridDim.x) * slices - 1) / (static_cast<int>(gridDim.x) * slices);
-  // Stretch i of this CTA is places [start_of(i), start_of(i + 1)).
+  const int stretches = static_cast<int>(gridDim.x) * slices;
+  int share = static_cast<int>(ceilf(static_cast<float>(total) * __frcp_rn(static_cast<float>(stretches))));
+  while (static_cast<long long>(share) * stretches < total) ++share;  // (where fp32 is too coarse)
+  // Stretch i of this CTA is places [start_of(i), start_of(i + 1)); its tiles are those whose places it has.
   auto start_of = [&](int i) {
     return static_cast<int>(min(static_cast<long long>(total), (static_cast<long long>(blockIdx.x) * slices + i) * share));
   };
   const int first = start_of(slice), last = start_of(slice + 1);
-  KvqCursor cur = {};  // the unit being computed
-  int unit_end = 0;    // its end in the row of all places
-  int left = 0;        // tiles of the stretch still to be fetched
+  KvqCursor cur = {};  // the unit being computed, from its tile cur.tile on
+  cur.end = total;
   if (first < last) {
-    // The stretch's tiles are those whose places it has; its first unit may have begun before it.
-    for (int b0 = 0, before = 0; b0 < p.B; b0 += 32) {
+    for (int b0 = 0, before = 0;; b0 += 32) {
       const int n = places(b0 + lane);
       int incl = n;
 #pragma unroll
@@ -321,29 +325,18 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         const int y = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += y;
       }
-      // places of this lane's sequence within the stretch, less its units' own among them
-      const int lo = max(first - (before + incl - n), 0), hi = min(last - (before + incl - n), n);
-      int mine = 0;
-      if (lo < hi) {
-        const int each = n / p.Hkv;
-        const int u0 = lo / each, u1 = hi / each;
-        mine = (u1 - u0) * (each - kKvqUnitCost) + max(hi - u1 * each - kKvqUnitCost, 0) - max(lo - u0 * each - kKvqUnitCost, 0);
-      }
-#pragma unroll
-      for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-      left += mine;
       const unsigned past = __ballot_sync(0xffffffffu, before + incl > first);
-      if (past && unit_end == 0) {  // the stretch begins in the first of these sequences
+      if (past) {  // (some sequence ends past it: first < total)
         const int l = __ffs(past) - 1, start = before + __shfl_sync(0xffffffffu, incl - n, l);
         cur.b = b0 + l;
         cur.s = kvq_seq<kTile>(p, cur.b);
         const int each = cur.s.tiles + kKvqUnitCost;
         cur.hk = (first - start) / each;
-        unit_end = start + (cur.hk + 1) * each;
-        cur.tile = max(first - (unit_end - each) - kKvqUnitCost, 0);
+        cur.end = start + (cur.hk + 1) * each;
+        cur.tile = max(first - (cur.end - cur.s.tiles), 0);
+        break;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
-      if (before >= last) break;
     }
   }
 
@@ -361,7 +354,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   const size_t n_rows = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_rows;
   KvqCursor pre = cur;  // the next tile this warp fetches
-  int pre_left = left;
+  int pre_left = cur.s.tiles - cur.tile;  // its unit's tiles from it on that the stretch has
+  pre_left = min(pre_left, last - (cur.end - pre_left));
   // its first row's codes at this lane's chunk, and its params (the lower half warp fetches the keys', the upper the
   // values')
   const uint8_t *k_from, *v_from, *p_from;
@@ -375,11 +369,6 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   };
   auto fetch = [&](int stage) {  // copies (or nothing) and one commit
     if (pre_left > 0) {
-      if (pre.tile == pre.s.tiles) {
-        pre.tile = 0;
-        kvq_next_unit<kTile>(p, pre);
-        aim();
-      }
       const int n = pre.s.L - (pre.s.start + pre.tile * kTile);  // valid rows (at least one)
       const uint32_t to = ring + stage * Shape::kStageBytes;
       const uint32_t p_to = to + 2 * Shape::kCodeBytes + (lane < 16 ? 0 : Shape::kParamBytes) + p_row * kGroups * 4;
@@ -407,12 +396,16 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
                                 in ? p_from + i * 64 * kGroups : reinterpret_cast<const uint8_t*>(p.k_params), in);
         }
       }
-      --pre_left;
       ++pre.tile;
       pre_row += kTile;
       k_from += kTile * kRowBytes;
       v_from += kTile * kRowBytes;
       p_from += kTile * kGroups * 4;
+      if (--pre_left == 0) {
+        kvq_next_unit<kTile>(p, pre);
+        pre_left = min(pre.s.tiles, last - (pre.end - pre.s.tiles));
+        if (pre_left > 0) aim();
+      }
     }
     cp_async_commit();
   };
@@ -440,9 +433,10 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   (void)n_q;
 
   int stage = 0;
-  for (int slot = 0; left > 0; slot = 1) {
+  for (int slot = 0; ; slot = 1) {
     // --- one piece: n_tiles tiles of unit (cur.b, cur.hk), from its tile cur.tile on
-    const int n_tiles = min(left, cur.s.tiles - cur.tile);
+    const int n_tiles = min(cur.s.tiles - cur.tile, last - (cur.end - cur.s.tiles + cur.tile));
+    if (n_tiles <= 0) break;  // (no stretch, or one that ends in a unit's own places)
     const bool whole = n_tiles == cur.s.tiles;
     // The unit's queries as B fragments: column g is row rt * 8 + g; the lane holds its dims that meet the words of a
     // key row that it reads, paired as the codes are, in units of 2^-up (4 bits: second and fourth nibbles 2^(4 - up),
@@ -738,13 +732,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         p.lse[lse_i] = kvq_lse(m[c], l[c]);
     }
     if (!whole && lane == 0 && rt == 0)
-      sh_piece[2 * slice + slot] = KvqPiece{cur.b * p.Hkv + cur.hk, cur.tile == 0, unit_end};
-    left -= n_tiles;
-    cur.tile = 0;
-    if (left > 0) {
-      kvq_next_unit<kTile>(p, cur);
-      unit_end += cur.s.tiles + kKvqUnitCost;
-    }
+      sh_piece[2 * slice + slot] = KvqPiece{cur.b * p.Hkv + cur.hk, cur.tile == 0, cur.end};
+    kvq_next_unit<kTile>(p, cur);
   }
   // Sequences without keys: o = 0, lse = -inf, shared out over the CTAs.
   for (int b = __any_sync(0xffffffffu, empty) ? blockIdx.x : p.B; b < p.B; b += gridDim.x) {
@@ -768,15 +757,18 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   for (int n = 0; heads; ++n) {
     const int i0 = __ffs(heads) - 1;
     heads &= heads - 1;
+    int r = (warp + 64 * kKvqWarps - n * R) % kKvqWarps;  // the chains' rows are the warps' in turn
+    if (r >= R) continue;
     const unsigned chain = have & (0xffffffffu << i0) & (heads ? (1u << (__ffs(heads) - 1)) - 1u : 0xffffffffu);
+    const int pieces = __popc(chain);  // the head, then the first pieces of the stretches after it
     const int unit = __shfl_sync(0xffffffffu, pc.unit, i0), end = __shfl_sync(0xffffffffu, pc.end, i0);
     const bool begins = __shfl_sync(0xffffffffu, pc.begins, i0), ends = end <= cta_end;
-    const int b = unit / p.Hkv, hk = unit % p.Hkv;
-    for (int r = (warp + 64 * kKvqWarps - n * R) % kKvqWarps; r < R; r += kKvqWarps) {  // rows of all chains in turn
-      // piece `lane` of row r: its warp is that of the stretch and the row's tile
+    const int b = unit / p.Hkv, hk = unit - b * p.Hkv;
+    for (; r < R; r += kKvqWarps) {
+      auto slot_of = [&](int s) { return s ? 0 : i0 & 1; };
+      auto warp_of = [&](int s) { return (i0 / 2 + s) * n_rt + r / 8; };  // piece s: its stretch's warp that had row r
       float2 ml = make_float2(kNone, 0.f);
-      if (chain >> lane & 1)
-        ml = *reinterpret_cast<const float2*>(piece_ml(lane & 1, (lane / 2) * n_rt + r / 8) + (r % 8) * 2);
+      if (lane < pieces) ml = *reinterpret_cast<const float2*>(piece_ml(slot_of(lane), warp_of(lane)) + (r % 8) * 2);
       float M = ml.x;
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -785,11 +777,11 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
       for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
       float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (unsigned c = chain; c; c &= c - 1) {
-        const int i = __ffs(c) - 1;
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float4 x = *reinterpret_cast<const float4*>(piece_o(i & 1, (i / 2) * n_rt + r / 8) + (r % 8) * 128 + lane * 4);
-        o4.x = fmaf(x.x, fi, o4.x), o4.y = fmaf(x.y, fi, o4.y), o4.z = fmaf(x.z, fi, o4.z), o4.w = fmaf(x.w, fi, o4.w);
+#pragma unroll 4
+      for (int s = 0; s < pieces; ++s) {
+        const float fs = __shfl_sync(0xffffffffu, f, s);
+        const float4 x = *reinterpret_cast<const float4*>(piece_o(slot_of(s), warp_of(s)) + (r % 8) * 128 + lane * 4);
+        o4.x = fmaf(x.x, fs, o4.x), o4.y = fmaf(x.y, fs, o4.y), o4.z = fmaf(x.z, fs, o4.z), o4.w = fmaf(x.w, fs, o4.w);
       }
       if (begins && ends) {
         const int q = p.row_i[r], h = hk * G + p.row_g[r];
