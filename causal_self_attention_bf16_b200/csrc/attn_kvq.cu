@@ -7,9 +7,10 @@
 // its value (|n s + z - x| <= s / 2). Every step is one correctly rounded fp32 operation, so the codes are defined
 // bit for bit. A group that holds a NaN or an infinity, or whose max - min overflows fp32, gets s = z = NaN.
 //
-// Write and read are HBM-bound copies with a few operations per value. A thread owns 8 of a row's 128 dims, of the
-// key and the value row alike: 16 threads cover a row, so a half-warp reads (writes) 256 contiguous bytes of bf16
-// and writes (reads) 64 or 128 contiguous bytes of codes.
+// Write and read are HBM-bound copies with a few operations per value. A thread owns 8 of a row's 128 dims, of the key
+// and the value row alike: 16 threads cover a row, so a half-warp reads (writes) 256 contiguous bytes of bf16 and
+// writes (reads) 64 or 128 contiguous bytes of codes. Rows are taken in the cache's order, the tokens of one head next
+// to each other, so that a warp's codes and params are one stretch of the cache.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,6 +36,17 @@ enum : uint32_t {
   kSiteKvqNew = 0xa0, kSiteKvqCodes = 0xa1, kSiteKvqParams = 0xa2, kSiteKvqOut = 0xa3
 };
 
+// Division by a number known on the host: n / d for n < 2^31 (the high half of n times 2^32 (2^shift / d - 1), rounded
+// up, plus n, shifted).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv(uint32_t d_ = 1) : d(d_), mul(0), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 struct CopyParams {
   const __nv_bfloat16* x[2];  // write: new key and value rows [B, T, H_kv, 128]
   __nv_bfloat16* y[2];        // read: key and value rows [B, T, H_kv, 128]
@@ -42,6 +54,7 @@ struct CopyParams {
   uint32_t* params[2];        // [B, H_kv, Tk, 128 / group] words: s in the low half, z in the high half
   const int* seqlens;         // [B]; read: null for rows from position 0 on
   int B, T, Hkv, Tk;
+  FastDiv by_T, by_Hkv;  // by T and by H_kv
 };
 
 // A kernel launched by launch_early: wait for the grid before it, and let the next one start up.
@@ -50,12 +63,17 @@ __device__ __forceinline__ void begin_early() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Row r of [B, T, H_kv] (token i of sequence b, head h): its cache row, or -1 where the token has no position.
-__device__ __forceinline__ long long cache_row(const CopyParams& p, int r) {
-  const int h = r % p.Hkv, bi = r / p.Hkv, b = bi / p.T, i = bi % p.T;
-  int pos = i;
+// Row r in the order [B, H_kv, T]: its row of [B, T, H_kv], its cache row, and whether the token has a position (both
+// counted in 31 bits).
+struct CopyRow {
+  uint32_t dense, cache;
+  bool there;
+};
+__device__ __forceinline__ CopyRow copy_row(const CopyParams& p, uint32_t r) {
+  const uint32_t bh = p.by_T.div(r), i = r - bh * p.T, b = p.by_Hkv.div(bh), h = bh - b * p.Hkv;
+  int pos = static_cast<int>(i);
   if (p.seqlens) pos += min(max(p.seqlens[b], 0), p.Tk) - p.T;
-  return pos < 0 ? -1 : (static_cast<long long>(b) * p.Hkv + h) * p.Tk + pos;
+  return {(b * p.T + i) * p.Hkv + h, bh * p.Tk + pos, pos >= 0};
 }
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
@@ -86,22 +104,46 @@ __device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t* sz) {
     *sz = 0x7fff7fffu;
     return make_uint2(0u, 0u);
   }
-  const uint32_t sbits = (__float_as_uint(__fdiv_rn(span, kLevels)) + 0xffffu) & 0xffff0000u;  // up to bf16
-  const float s = __uint_as_float(sbits);
-  *sz = (sbits >> 16) | (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
-  uint32_t n[8];
+  // Quotients by Markstein's method (IBM J. Res. Dev. 34, 1990): with y = 1 / b rounded to nearest and q = a y, the
+  // sum q + (a - q b) y, the remainder exact, is a / b rounded to nearest. Nothing less will do: bf16 numbers over a
+  // bf16 scale lie on ties often (one in 50 at 4 bits). The compiler's divisions took 1.6 times as long. Added to
+  // 1.5 * 2^23 a quotient is rounded to an integer in the sum's low bits.
+  constexpr float kMagic = 12582912.f, kInverse = 1.f / kLevels;
+  float quotient = span * kInverse;
+  quotient = fmaf(fmaf(-quotient, kLevels, span), kInverse, quotient);
+  uint32_t sbits = (__float_as_uint(quotient) + 0xffffu) & 0xffff0000u;  // up to bf16
+  uint32_t t[8];
+  if (span >= 0x1p-80f && span <= 0x1p100f) {
+    const float s = __uint_as_float(sbits), y = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = (i & 1) ? hi_f32(w[i / 2]) : lo_f32(w[i / 2]);
-    const float q = sbits ? __fdiv_rn(x - z, s) : 0.f;
-    n[i] = static_cast<uint32_t>(fminf(rintf(q), kLevels));
+    for (int i = 0; i < 8; ++i) {
+      const float a = ((i & 1) ? hi_f32(w[i / 2]) : lo_f32(w[i / 2])) - z;
+      const float q = a * y;
+      t[i] = __float_as_uint(fmaf(fmaf(-q, s, a), y, q) + kMagic);
+    }
+  } else {  // an inverse or a remainder may not be a normal number; or a constant group, whose scale and codes are 0
+    sbits = (__float_as_uint(__fdiv_rn(span, kLevels)) + 0xffffu) & 0xffff0000u;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t word = i < 2 ? w[0] : i < 4 ? w[1] : i < 6 ? w[2] : w[3];
+      const float a = ((i & 1) ? hi_f32(word) : lo_f32(word)) - z;
+      const uint32_t n = __float_as_uint(fminf(sbits ? __fdiv_rn(a, __uint_as_float(sbits)) : 0.f, kLevels) + kMagic);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i == j) t[j] = n;
+    }
   }
+  *sz = (sbits >> 16) | (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
+  // t = 0x4b400000 + n, of which only the low bits are wanted
   uint2 c = make_uint2(0u, 0u);
+  if constexpr (kBits == 4) {
+    uint32_t u = t[7];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (kBits == 4) c.x |= n[i] << (4 * i);
-    else if (i < 4) c.x |= n[i] << (8 * i);
-    else c.y |= n[i] << (8 * (i - 4));
+    for (int i = 6; i >= 0; --i) u = u * 16u + t[i];
+    c.x = u - 0x4b400000u * 0x11111111u;
+  } else {
+    c.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+    c.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
   }
   return c;
 }
@@ -110,31 +152,31 @@ template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(const CopyParams p) {
   begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
-  const int c = threadIdx.x % kChunks;
-  const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
-  const unsigned long long n_new = static_cast<unsigned long long>(rows) * 128;
-  const unsigned long long n_cache = static_cast<unsigned long long>(p.B) * p.Hkv * p.Tk;
+  const uint32_t c = threadIdx.x % kChunks, r = blockIdx.x * (kCopyThreads / kChunks) + threadIdx.x / kChunks;
+  const uint32_t rows = static_cast<uint32_t>(p.B) * p.T * p.Hkv;
+  const size_t n_new = static_cast<size_t>(rows) * 128, n_cache = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_new, (void)n_cache;
-  const long long r = static_cast<long long>(blockIdx.x) * (kCopyThreads / kChunks) + threadIdx.x / kChunks;
-  const long long row = r < rows ? cache_row(p, static_cast<int>(r)) : -1;  // every lane stays for the shuffles
+  const bool live = r < rows;  // (every lane stays for the shuffles)
+  const CopyRow at = copy_row(p, live ? r : 0u);
+  const size_t from = at.dense * size_t{128} + 8 * c;
   uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (live && ATTN_IN_RANGE(from, 8, n_new, kSiteKvqNew, &g_kvq_error)) {
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-    if (row >= 0 && ATTN_IN_RANGE(r * 128 + 8 * c, 8, n_new, kSiteKvqNew, &g_kvq_error))
-      raw[t] = *reinterpret_cast<const uint4*>(p.x[t] + r * 128 + 8 * c);
+    for (int t = 0; t < 2; ++t)  // (read whether the token has a position or not: that is not known yet)
+      raw[t] = *reinterpret_cast<const uint4*>(p.x[t] + from);
+  }
+  const size_t to = at.cache * static_cast<size_t>(kRowBytes) + c * kBits;
+  const size_t sz_to = at.cache * static_cast<size_t>(kGroups) + 8 * c / kGroup;
+  const bool write = live && at.there && ATTN_IN_RANGE(to, kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error) &&
+                     ATTN_IN_RANGE(sz_to, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     uint32_t sz;
     const uint2 codes = quantise8<kBits, kGroup>(raw[t], &sz);
-    if (row < 0) continue;
-    if (ATTN_IN_RANGE(row * kRowBytes + c * kBits, kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error)) {
-      uint8_t* to = p.codes[t] + row * kRowBytes + c * kBits;
-      if constexpr (kBits == 4) *reinterpret_cast<uint32_t*>(to) = codes.x;
-      else *reinterpret_cast<uint2*>(to) = codes;
-    }
-    if ((8 * c) % kGroup == 0 &&
-        ATTN_IN_RANGE(row * kGroups + 8 * c / kGroup, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error))
-      p.params[t][row * kGroups + 8 * c / kGroup] = sz;
+    if (!write) continue;
+    if constexpr (kBits == 4) *reinterpret_cast<uint32_t*>(p.codes[t] + to) = codes.x;
+    else *reinterpret_cast<uint2*>(p.codes[t] + to) = codes;
+    if ((8 * c) % kGroup == 0) p.params[t][sz_to] = sz;
   }
 }
 
@@ -142,44 +184,46 @@ template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(const CopyParams p) {
   begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
-  const int c = threadIdx.x % kChunks;
-  const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
-  const unsigned long long n_out = static_cast<unsigned long long>(rows) * 128;
-  const unsigned long long n_cache = static_cast<unsigned long long>(p.B) * p.Hkv * p.Tk;
+  const uint32_t c = threadIdx.x % kChunks, r = blockIdx.x * (kCopyThreads / kChunks) + threadIdx.x / kChunks;
+  const uint32_t rows = static_cast<uint32_t>(p.B) * p.T * p.Hkv;
+  const size_t n_out = static_cast<size_t>(rows) * 128, n_cache = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_out, (void)n_cache;
-  const long long r = static_cast<long long>(blockIdx.x) * (kCopyThreads / kChunks) + threadIdx.x / kChunks;
   if (r >= rows) return;
-  const long long row = cache_row(p, static_cast<int>(r));
+  const CopyRow at = copy_row(p, r);
   uint2 codes[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
   uint32_t sz[2] = {0u, 0u};  // s = z = 0: rows without a position read as 0
-  if (row >= 0) {
+  const size_t from = at.cache * static_cast<size_t>(kRowBytes) + c * kBits;
+  const size_t sz_from = at.cache * static_cast<size_t>(kGroups) + 8 * c / kGroup;
+  if (at.there && ATTN_IN_RANGE(from, kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error) &&
+      ATTN_IN_RANGE(sz_from, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error)) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (ATTN_IN_RANGE(row * kRowBytes + c * kBits, kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error)) {
-        const uint8_t* from = p.codes[t] + row * kRowBytes + c * kBits;
-        if constexpr (kBits == 4) codes[t].x = *reinterpret_cast<const uint32_t*>(from);
-        else codes[t] = *reinterpret_cast<const uint2*>(from);
-      }
-      if (ATTN_IN_RANGE(row * kGroups + 8 * c / kGroup, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error))
-        sz[t] = p.params[t][row * kGroups + 8 * c / kGroup];
+      if constexpr (kBits == 4) codes[t].x = *reinterpret_cast<const uint32_t*>(p.codes[t] + from);
+      else codes[t] = *reinterpret_cast<const uint2*>(p.codes[t] + from);
+      sz[t] = p.params[t][sz_from];
     }
   }
+  const size_t to = at.dense * size_t{128} + 8 * c;
+  if (!ATTN_IN_RANGE(to, 8, n_out, kSiteKvqOut, &g_kvq_error)) return;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const float s = lo_f32(sz[t]), z = hi_f32(sz[t]);
+    // Byte b of a word as the bits of 2^23 + b, less 2^23: full-rate operations, where the integer conversions are
+    // made at a quarter of the rate.
+    auto number = [](uint32_t bytes, int i) {
+      return __uint_as_float(__byte_perm(bytes, 0x4b000000u, 0x7440 + i)) - 8388608.f;
+    };
+    uint32_t even = 0, odd = 0;  // 4 bits: the even and the odd dims' codes, a byte each
+    if constexpr (kBits == 4) even = codes[t].x & 0x0f0f0f0fu, odd = (codes[t].x >> 4) & 0x0f0f0f0fu;
     uint32_t out[4];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      uint32_t n0, n1;
-      if constexpr (kBits == 4) n0 = (codes[t].x >> (4 * i)) & 15u, n1 = (codes[t].x >> (4 * i + 4)) & 15u;
-      else {
-        const uint32_t w = i < 4 ? codes[t].x : codes[t].y;
-        n0 = (w >> (8 * (i % 4))) & 255u, n1 = (w >> (8 * (i % 4) + 8)) & 255u;
-      }
-      out[i / 2] = as_u32(__floats2bfloat162_rn(fmaf(static_cast<float>(n0), s, z), fmaf(static_cast<float>(n1), s, z)));
+    for (int i = 0; i < 4; ++i) {  // dims 2 i and 2 i + 1
+      float n0, n1;
+      if constexpr (kBits == 4) n0 = number(even, i), n1 = number(odd, i);
+      else n0 = number(i < 2 ? codes[t].x : codes[t].y, 2 * (i % 2)), n1 = number(i < 2 ? codes[t].x : codes[t].y, 2 * (i % 2) + 1);
+      out[i] = as_u32(__floats2bfloat162_rn(fmaf(n0, s, z), fmaf(n1, s, z)));
     }
-    if (ATTN_IN_RANGE(r * 128 + 8 * c, 8, n_out, kSiteKvqOut, &g_kvq_error))
-      *reinterpret_cast<uint4*>(p.y[t] + r * 128 + 8 * c) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<uint4*>(p.y[t] + to) = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
@@ -223,9 +267,9 @@ attn_status check_copy(int B, int T, int H_kv, int Tk, int D, int bits, int grou
   if (B < 1 || T < 1 || H_kv < 1 || Tk < 1) return ATTN_ERR_INVALID_ARG;
   const attn_status st = check_format(D, bits, group);
   if (st != ATTN_OK) return st;
-  // rows and cache rows are counted in 31 and 40 bits; byte offsets in 64
+  // rows and cache rows are counted in 31 bits, byte offsets in 64
   if (static_cast<long long>(B) * T > 0x7fffffffLL / H_kv) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * H_kv > (1LL << 40) / Tk) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * H_kv > 0x7fffffffLL / Tk) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -283,8 +327,9 @@ attn_status check_decode(int B, int H, int Hkv, int Tq, int Tk, int D, int bits,
   if (st != ATTN_OK) return st;
   if ((H / Hkv) * static_cast<long long>(Tq) > attn::kKvqMaxRows) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H * Tq > 0x7fffffffLL / 8) return ATTN_ERR_UNSUPPORTED;
-  // the units' tiles (16 keys or more) are counted in 30 bits
-  if (static_cast<long long>(B) * Hkv > (1LL << 30) / (Tk / 16 + 1)) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL / Tk) return ATTN_ERR_UNSUPPORTED;  // cache rows, as for write and read
+  // the row of all places (a unit's tiles, 16 keys or more each, and a few) is counted in 30 bits
+  if (static_cast<long long>(B) * Hkv > (1LL << 30) / (Tk / 16 + 1 + attn::kKvqUnitCost)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -343,6 +388,7 @@ attn_status attn_kvq_write(const void* k, const void* v, void* k_codes, void* k_
   p.params[1] = static_cast<uint32_t*>(v_params);
   p.seqlens = cache_seqlens;
   p.B = B, p.T = T, p.Hkv = H_kv, p.Tk = Tk;
+  p.by_T = FastDiv(T), p.by_Hkv = FastDiv(H_kv);
   return launch_copy(true, p, bits, group, stream);
 }
 
@@ -372,6 +418,7 @@ attn_status attn_kvq_read(const void* k_codes, const void* k_params, const void*
   p.params[1] = const_cast<uint32_t*>(static_cast<const uint32_t*>(v_params));
   p.seqlens = cache_seqlens;
   p.B = B, p.T = T, p.Hkv = H_kv, p.Tk = Tk;
+  p.by_T = FastDiv(T), p.by_Hkv = FastDiv(H_kv);
   return launch_copy(false, p, bits, group, stream);
 }
 
