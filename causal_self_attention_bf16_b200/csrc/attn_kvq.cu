@@ -7,10 +7,10 @@
 // its value (|n s + z - x| <= s / 2). Every step is one correctly rounded fp32 operation, so the codes are defined
 // bit for bit. A group that holds a NaN or an infinity, or whose max - min overflows fp32, gets s = z = NaN.
 //
-// Write and read are HBM-bound copies with a few operations per value. A thread owns 8 of a row's 128 dims, of the key
-// and the value row alike: 16 threads cover a row, so a half-warp reads (writes) 256 contiguous bytes of bf16 and
-// writes (reads) 64 or 128 contiguous bytes of codes. Rows are taken in the cache's order, the tokens of one head next
-// to each other, so that a warp's codes and params are one stretch of the cache.
+// Write and read are HBM-bound copies with a few operations per value. A thread owns some of a row's 128 dims, of the
+// key and the value row alike: 16 of them in write, whose work per group (minimum, scale, inverse) is then shared by
+// twice as many values as with 8, and 8 in read. Rows are taken in the cache's order, the tokens of one head next to
+// each other, so that a warp's codes and params are one stretch of the cache.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,7 +31,7 @@ namespace {
 using attn::g_cuda_error;
 
 constexpr int kCopyThreads = 256;
-constexpr int kChunks = 16;  // threads per row, 8 dims each
+constexpr int kReadLanes = 16, kWriteLanes = 8;  // threads per row
 enum : uint32_t {
   kSiteKvqNew = 0xa0, kSiteKvqCodes = 0xa1, kSiteKvqParams = 0xa2, kSiteKvqOut = 0xa3
 };
@@ -81,102 +81,111 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpr
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Quantise this thread's 8 dims, in a group that spans kGroup / 8 neighbouring threads. Returns the codes
-// (4 bits: word 0, nibble i = dim i; 8 bits: words 0 and 1, byte i = dim i) and the group's (s, z) word.
+// Quantise this thread's 16 dims (bf16 pairs w), in a group that spans kGroup / 16 neighbouring threads: their codes,
+// packed in dim order, and the group's (s, z) word.
 template <int kBits, int kGroup>
-__device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t* sz) {
+__device__ __forceinline__ void quantise16(const uint32_t (&w)[8], uint32_t (&codes)[kBits / 2], uint32_t* sz) {
   constexpr float kLevels = kBits == 4 ? 15.f : 255.f;
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   // min and max of bf16 pairs; a NaN anywhere in the group wins
-  __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(as_bf162(w[0]), as_bf162(w[1])),
-                                  __hmin2_nan(as_bf162(w[2]), as_bf162(w[3])));
-  __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(as_bf162(w[0]), as_bf162(w[1])),
-                                  __hmax2_nan(as_bf162(w[2]), as_bf162(w[3])));
+  __nv_bfloat162 mn = as_bf162(w[0]), mx = as_bf162(w[0]);
 #pragma unroll
-  for (int m = 1; m < kGroup / 8; m <<= 1) {
+  for (int i = 1; i < 8; ++i) mn = __hmin2_nan(mn, as_bf162(w[i])), mx = __hmax2_nan(mx, as_bf162(w[i]));
+#pragma unroll
+  for (int m = 1; m < kGroup / 16; m <<= 1) {
     mn = __hmin2_nan(mn, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mn), m)));
     mx = __hmax2_nan(mx, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(mx), m)));
   }
   const __nv_bfloat16 zb = __hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn));
   const float z = __bfloat162float(zb);
   const float span = __bfloat162float(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx))) - z;
-  if (!(span < INFINITY)) {  // a NaN or an infinity in the group, or a range past fp32: NaN throughout
-    *sz = 0x7fff7fffu;
-    return make_uint2(0u, 0u);
-  }
   // Quotients by Markstein's method (IBM J. Res. Dev. 34, 1990): with y = 1 / b rounded to nearest and q = a y, the
   // sum q + (a - q b) y, the remainder exact, is a / b rounded to nearest. Nothing less will do: bf16 numbers over a
   // bf16 scale lie on ties often (one in 50 at 4 bits). The compiler's divisions took 1.6 times as long. Added to
   // 1.5 * 2^23 a quotient is rounded to an integer in the sum's low bits.
   constexpr float kMagic = 12582912.f, kInverse = 1.f / kLevels;
-  float quotient = span * kInverse;
-  quotient = fmaf(fmaf(-quotient, kLevels, span), kInverse, quotient);
-  uint32_t sbits = (__float_as_uint(quotient) + 0xffffu) & 0xffff0000u;  // up to bf16
-  uint32_t t[8];
+  uint32_t t[16];
   if (span >= 0x1p-80f && span <= 0x1p100f) {
+    float quotient = span * kInverse;
+    quotient = fmaf(fmaf(-quotient, kLevels, span), kInverse, quotient);
+    const uint32_t sbits = (__float_as_uint(quotient) + 0xffffu) & 0xffff0000u;  // up to bf16
     const float s = __uint_as_float(sbits), y = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const float a = ((i & 1) ? hi_f32(w[i / 2]) : lo_f32(w[i / 2])) - z;
       const float q = a * y;
       t[i] = __float_as_uint(fmaf(fmaf(-q, s, a), y, q) + kMagic);
     }
-  } else {  // an inverse or a remainder may not be a normal number; or a constant group, whose scale and codes are 0
-    sbits = (__float_as_uint(__fdiv_rn(span, kLevels)) + 0xffffu) & 0xffff0000u;
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t word = i < 2 ? w[0] : i < 4 ? w[1] : i < 6 ? w[2] : w[3];
-      const float a = ((i & 1) ? hi_f32(word) : lo_f32(word)) - z;
-      const uint32_t n = __float_as_uint(fminf(sbits ? __fdiv_rn(a, __uint_as_float(sbits)) : 0.f, kLevels) + kMagic);
+    *sz = (sbits >> 16) | (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
+  } else if (span < INFINITY) {  // an inverse or a remainder may not be a normal number; or a constant group: s and n are 0
+    const uint32_t sbits = (__float_as_uint(__fdiv_rn(span, kLevels)) + 0xffffu) & 0xffff0000u;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i == j) t[j] = n;
+    for (int i = 0; i < 16; ++i) t[i] = __float_as_uint(kMagic);
+    if (sbits) {
+#pragma unroll 1
+      for (int i = 0; i < 16; ++i) {
+        uint32_t word = w[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) word = i / 2 == j ? w[j] : word;
+        const float a = ((i & 1) ? hi_f32(word) : lo_f32(word)) - z;
+        const uint32_t n = __float_as_uint(fminf(__fdiv_rn(a, __uint_as_float(sbits)), kLevels) + kMagic);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) t[j] = i == j ? n : t[j];
+      }
+    }
+    *sz = (sbits >> 16) | (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
+  } else {  // a NaN or an infinity in the group, or a range past fp32: NaN throughout
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = __float_as_uint(kMagic);
+    *sz = 0x7fff7fffu;
+  }
+  // t = 0x4b400000 + n, of which only the low bits are wanted
+#pragma unroll
+  for (int i = 0; i < kBits / 2; ++i) {
+    if constexpr (kBits == 4) {
+      uint32_t u = t[8 * i + 7];
+#pragma unroll
+      for (int j = 6; j >= 0; --j) u = u * 16u + t[8 * i + j];
+      codes[i] = u - 0x4b400000u * 0x11111111u;
+    } else {
+      codes[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040), __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040), 0x5410);
     }
   }
-  *sz = (sbits >> 16) | (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
-  // t = 0x4b400000 + n, of which only the low bits are wanted
-  uint2 c = make_uint2(0u, 0u);
-  if constexpr (kBits == 4) {
-    uint32_t u = t[7];
-#pragma unroll
-    for (int i = 6; i >= 0; --i) u = u * 16u + t[i];
-    c.x = u - 0x4b400000u * 0x11111111u;
-  } else {
-    c.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
-    c.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
-  }
-  return c;
 }
 
 template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(const CopyParams p) {
   begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
-  const uint32_t c = threadIdx.x % kChunks, r = blockIdx.x * (kCopyThreads / kChunks) + threadIdx.x / kChunks;
+  const uint32_t c = threadIdx.x % kWriteLanes, r = blockIdx.x * (kCopyThreads / kWriteLanes) + threadIdx.x / kWriteLanes;
   const uint32_t rows = static_cast<uint32_t>(p.B) * p.T * p.Hkv;
   const size_t n_new = static_cast<size_t>(rows) * 128, n_cache = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_new, (void)n_cache;
   const bool live = r < rows;  // (every lane stays for the shuffles)
   const CopyRow at = copy_row(p, live ? r : 0u);
-  const size_t from = at.dense * size_t{128} + 8 * c;
-  uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  if (live && ATTN_IN_RANGE(from, 8, n_new, kSiteKvqNew, &g_kvq_error)) {
+  const size_t from = at.dense * size_t{128} + 16 * c;
+  uint32_t raw[2][8] = {};
+  if (live && ATTN_IN_RANGE(from, 16, n_new, kSiteKvqNew, &g_kvq_error)) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)  // (read whether the token has a position or not: that is not known yet)
-      raw[t] = *reinterpret_cast<const uint4*>(p.x[t] + from);
+    for (int t = 0; t < 2; ++t) {  // (read whether the token has a position or not: that is not known yet)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 u = reinterpret_cast<const uint4*>(p.x[t] + from)[i];
+        raw[t][4 * i] = u.x, raw[t][4 * i + 1] = u.y, raw[t][4 * i + 2] = u.z, raw[t][4 * i + 3] = u.w;
+      }
+    }
   }
-  const size_t to = at.cache * static_cast<size_t>(kRowBytes) + c * kBits;
-  const size_t sz_to = at.cache * static_cast<size_t>(kGroups) + 8 * c / kGroup;
-  const bool write = live && at.there && ATTN_IN_RANGE(to, kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error) &&
+  const size_t to = at.cache * static_cast<size_t>(kRowBytes) + c * (2 * kBits);
+  const size_t sz_to = at.cache * static_cast<size_t>(kGroups) + 16 * c / kGroup;
+  const bool write = live && at.there && ATTN_IN_RANGE(to, 2 * kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error) &&
                      ATTN_IN_RANGE(sz_to, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    uint32_t sz;
-    const uint2 codes = quantise8<kBits, kGroup>(raw[t], &sz);
+    uint32_t sz, codes[kBits / 2];
+    quantise16<kBits, kGroup>(raw[t], codes, &sz);
     if (!write) continue;
-    if constexpr (kBits == 4) *reinterpret_cast<uint32_t*>(p.codes[t] + to) = codes.x;
-    else *reinterpret_cast<uint2*>(p.codes[t] + to) = codes;
-    if ((8 * c) % kGroup == 0) p.params[t][sz_to] = sz;
+    if constexpr (kBits == 4) *reinterpret_cast<uint2*>(p.codes[t] + to) = make_uint2(codes[0], codes[1]);
+    else *reinterpret_cast<uint4*>(p.codes[t] + to) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+    if ((16 * c) % kGroup == 0) p.params[t][sz_to] = sz;
   }
 }
 
@@ -184,7 +193,7 @@ template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(const CopyParams p) {
   begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
-  const uint32_t c = threadIdx.x % kChunks, r = blockIdx.x * (kCopyThreads / kChunks) + threadIdx.x / kChunks;
+  const uint32_t c = threadIdx.x % kReadLanes, r = blockIdx.x * (kCopyThreads / kReadLanes) + threadIdx.x / kReadLanes;
   const uint32_t rows = static_cast<uint32_t>(p.B) * p.T * p.Hkv;
   const size_t n_out = static_cast<size_t>(rows) * 128, n_cache = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_out, (void)n_cache;
@@ -308,7 +317,8 @@ cudaError_t launch_early(void (*kernel)(P), dim3 grid, int threads, size_t smem,
 
 attn_status launch_copy(bool write, const CopyParams& p, int bits, int group, void* stream) {
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
-  const unsigned grid = static_cast<unsigned>((rows + kCopyThreads / kChunks - 1) / (kCopyThreads / kChunks));
+  const int per_block = kCopyThreads / (write ? kWriteLanes : kReadLanes);
+  const unsigned grid = static_cast<unsigned>((rows + per_block - 1) / per_block);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   with_format(bits, group, [&](auto b, auto g) {

@@ -116,6 +116,34 @@ def test_write_unusual_rows(bits, group):
     check_row(-x[0, :, 0].cpu(), cache.v_codes[0, 0], cache.v_params[0, 0], bits, group, "v")
 
 
+@pytest.mark.parametrize("bits,group", BITS_GROUPS)
+def test_write_codes_are_the_formula_bit_for_bit(bits, group):
+    """Codes and params equal the format's fp32 operations made one by one on the CPU (IEEE divisions), ties included:
+    rows of every size (2^-90 to 2^90), on coarse grids where ties are common, and each of the 128 scale mantissas."""
+    g = torch.Generator().manual_seed(100 * bits + group)
+    x = torch.randn(4000, 128, generator=g) * torch.exp2(torch.randint(-90, 91, (4000, 1), generator=g).float())
+    grid = torch.randint(-300, 300, (3000, 128), generator=g).float() * torch.exp2(torch.randint(-20, 20, (3000, 1), generator=g).float())
+    # a span of m * 2^k * levels has the scale m * 2^k: m in [1, 2) in steps of 2^-7, the rest of the group on halves
+    m = 1 + torch.arange(128).float() / 128
+    lanes = torch.arange(128) % group
+    steps = torch.where(lanes == 0, torch.tensor(0.0), torch.where(lanes == 1, torch.tensor(float(2 ** bits - 1)),
+                                                                  (lanes % (2 ** bits - 1)).float() + 0.5))
+    halves = (m[:, None] * steps[None, :])
+    x = torch.cat([x, grid, halves, x[:500] + 1000 * x[:500, :1]]).to(torch.bfloat16)
+    levels = float(2 ** bits - 1)
+    r = x.float().reshape(-1, 128 // group, group)
+    z = r.amin(-1, keepdim=True)
+    span = r.amax(-1, keepdim=True) - z
+    s = ((span / torch.full_like(span, levels)).view(torch.int32) + 0xFFFF & -65536).view(torch.float32)
+    n = torch.where(s > 0, torch.round((r - z) / s), torch.zeros_like(r)).clamp(max=levels).reshape(-1, 128).long()
+    rows = x.shape[0]
+    cache = attn.kvq_cache(1, 1, rows, bits, group)
+    attn.kvq_write(cache, x.reshape(1, rows, 1, 128).cuda(), (-x).reshape(1, rows, 1, 128).cuda(), ints([rows]))
+    clean()
+    assert np.array_equal(unpack_codes(cache.k_codes[0, 0].cpu().numpy(), bits), n.numpy())
+    assert torch.equal(cache.k_params[0, 0].cpu().float(), torch.cat([s, z], -1))
+
+
 def test_write_many_rows():
     """Enough rows for many blocks, checked against the oracle on a sample and for every row's error bound."""
     B, T, Hkv, bits, group = 3, 701, 10, 4, 64
