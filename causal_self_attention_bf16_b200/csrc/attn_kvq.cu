@@ -30,7 +30,9 @@ namespace {
 
 using attn::g_cuda_error;
 
-constexpr int kCopyThreads = 256;
+// Threads per block: 256 made write 3 % slower (its registers leave no whole number of such blocks), 128 made read 25 %
+// slower.
+constexpr int kReadThreads = 256, kWriteThreads = 128;
 constexpr int kReadLanes = 16, kWriteLanes = 8;  // threads per row
 enum : uint32_t {
   kSiteKvqNew = 0xa0, kSiteKvqCodes = 0xa1, kSiteKvqParams = 0xa2, kSiteKvqOut = 0xa3
@@ -81,6 +83,31 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpr
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Two fp32 operations in one instruction, each rounded to nearest.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // Quantise this thread's 16 dims (bf16 pairs w), in a group that spans kGroup / 16 neighbouring threads: their codes,
 // packed in dim order, and the group's (s, z) word.
 template <int kBits, int kGroup>
@@ -109,11 +136,12 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], uint32_t (&co
     quotient = fmaf(fmaf(-quotient, kLevels, span), kInverse, quotient);
     const uint32_t sbits = (__float_as_uint(quotient) + 0xffffu) & 0xffff0000u;  // up to bf16
     const float s = __uint_as_float(sbits), y = __frcp_rn(s);
+    const F2 y2 = f2(y, y), minus_s = f2(-s, -s), minus_z = f2(-z, -z), magic = f2(kMagic, kMagic);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float a = ((i & 1) ? hi_f32(w[i / 2]) : lo_f32(w[i / 2])) - z;
-      const float q = a * y;
-      t[i] = __float_as_uint(fmaf(fmaf(-q, s, a), y, q) + kMagic);
+    for (int i = 0; i < 8; ++i) {
+      const F2 a = add2(f2(lo_f32(w[i]), hi_f32(w[i])), minus_z), q = mul2(a, y2);
+      const F2 n = add2(fma2(fma2(q, minus_s, a), y2, q), magic);
+      t[2 * i] = static_cast<uint32_t>(n.v), t[2 * i + 1] = static_cast<uint32_t>(n.v >> 32);
     }
     *sz = (sbits >> 16) | (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
   } else if (span < INFINITY) {  // an inverse or a remainder may not be a normal number; or a constant group: s and n are 0
@@ -144,7 +172,7 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], uint32_t (&co
     if constexpr (kBits == 4) {
       uint32_t u = t[8 * i + 7];
 #pragma unroll
-      for (int j = 6; j >= 0; --j) u = u * 16u + t[8 * i + j];
+      for (int j = 6; j >= 0; --j) u = (u << 4) + t[8 * i + j];
       codes[i] = u - 0x4b400000u * 0x11111111u;
     } else {
       codes[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040), __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040), 0x5410);
@@ -153,10 +181,10 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], uint32_t (&co
 }
 
 template <int kBits, int kGroup>
-__global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(const CopyParams p) {
+__global__ void __launch_bounds__(kWriteThreads) kvq_write_kernel(const CopyParams p) {
   begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
-  const uint32_t c = threadIdx.x % kWriteLanes, r = blockIdx.x * (kCopyThreads / kWriteLanes) + threadIdx.x / kWriteLanes;
+  const uint32_t c = threadIdx.x % kWriteLanes, r = blockIdx.x * (kWriteThreads / kWriteLanes) + threadIdx.x / kWriteLanes;
   const uint32_t rows = static_cast<uint32_t>(p.B) * p.T * p.Hkv;
   const size_t n_new = static_cast<size_t>(rows) * 128, n_cache = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_new, (void)n_cache;
@@ -190,10 +218,10 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(const CopyParam
 }
 
 template <int kBits, int kGroup>
-__global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(const CopyParams p) {
+__global__ void __launch_bounds__(kReadThreads) kvq_read_kernel(const CopyParams p) {
   begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
-  const uint32_t c = threadIdx.x % kReadLanes, r = blockIdx.x * (kCopyThreads / kReadLanes) + threadIdx.x / kReadLanes;
+  const uint32_t c = threadIdx.x % kReadLanes, r = blockIdx.x * (kReadThreads / kReadLanes) + threadIdx.x / kReadLanes;
   const uint32_t rows = static_cast<uint32_t>(p.B) * p.T * p.Hkv;
   const size_t n_out = static_cast<size_t>(rows) * 128, n_cache = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_out, (void)n_cache;
@@ -317,13 +345,13 @@ cudaError_t launch_early(void (*kernel)(P), dim3 grid, int threads, size_t smem,
 
 attn_status launch_copy(bool write, const CopyParams& p, int bits, int group, void* stream) {
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
-  const int per_block = kCopyThreads / (write ? kWriteLanes : kReadLanes);
+  const int threads = write ? kWriteThreads : kReadThreads, per_block = threads / (write ? kWriteLanes : kReadLanes);
   const unsigned grid = static_cast<unsigned>((rows + per_block - 1) / per_block);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   with_format(bits, group, [&](auto b, auto g) {
     e = launch_early(write ? kvq_write_kernel<b.value, g.value> : kvq_read_kernel<b.value, g.value>, dim3(grid),
-                     kCopyThreads, 0, s, p);
+                     threads, 0, s, p);
   });
   if (e != cudaSuccess) return cuda_fail(e, write ? "kvq_write_kernel launch" : "kvq_read_kernel launch");
   return ATTN_OK;
