@@ -12,6 +12,7 @@ include/attn.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import NamedTuple, Optional, Tuple
@@ -372,27 +373,49 @@ def kvq_cache(B: int, H_kv: int, Tk: int, bits: int = 4, group: int = 64, device
 def _check_kvq(cache):
     """Check the cache's four tensors (all on one device). Returns (their pointers, B, H_kv, Tk, bits, group,
     device)."""
-    if not isinstance(cache, (tuple, list)) or len(cache) != 4 or not all(isinstance(t, torch.Tensor) for t in cache):
+    if not isinstance(cache, (tuple, list)) or len(cache) != 4:
         raise ValueError("cache must be a KVQCache or a tuple (k_codes, k_params, v_codes, v_params)")
+    for t in cache:
+        if not isinstance(t, torch.Tensor):
+            raise ValueError("cache must hold four tensors (k_codes, k_params, v_codes, v_params)")
     kc, kp, vc, vp = cache
     dev, cs, ps = kc.device, kc.shape, kp.shape
-    if len(cs) != 4 or cs[3] not in (64, 128) or min(cs) < 1:
+    if len(cs) != 4 or cs[3] not in (64, 128) or 0 in cs:
         raise ValueError(f"k_codes has shape {tuple(cs)}; expected [B, H_kv, Tk, 64] (4 bits) or [.., 128] (8 bits)")
     if len(ps) != 5 or ps[:3] != cs[:3] or ps[3] not in (1, 2, 4) or ps[4] != 2:
         raise ValueError(f"k_params has shape {tuple(ps)}; expected [{cs[0]}, {cs[1]}, {cs[2]}, 128 // group, 2]")
-    for name, t, shape, dtype in (("k_codes", kc, cs, torch.uint8), ("k_params", kp, ps, torch.bfloat16),
-                                  ("v_codes", vc, cs, torch.uint8), ("v_params", vp, ps, torch.bfloat16)):
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}; every tensor of one call must be on {dev}")
-    return (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), cs[0], cs[1], cs[2], cs[3] // 16, 128 // ps[3], dev
+    if not (kc.dtype == vc.dtype == torch.uint8 and kp.dtype == vp.dtype == torch.bfloat16 and vc.shape == cs
+            and vp.shape == ps and kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous()
+            and vp.is_contiguous() and kp.device == dev and vc.device == dev and vp.device == dev):
+        for name, t, shape, dtype in (("k_codes", kc, cs, torch.uint8), ("k_params", kp, ps, torch.bfloat16),
+                                      ("v_codes", vc, cs, torch.uint8), ("v_params", vp, ps, torch.bfloat16)):
+            if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor")
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}; every tensor of one call must be on {dev}")
+    return ((kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), cs[0], cs[1], cs[2], cs[3] // 16,
+            128 // ps[3], dev)
 
 
 def _check_seqlens(cache_seqlens, B: int, dev: torch.device):
     if (not isinstance(cache_seqlens, torch.Tensor) or cache_seqlens.dtype != torch.int32 or
-            tuple(cache_seqlens.shape) != (B,) or cache_seqlens.device != dev or not cache_seqlens.is_contiguous()):
+            cache_seqlens.shape != (B,) or cache_seqlens.device != dev or not cache_seqlens.is_contiguous()):
         raise ValueError("cache_seqlens must be a contiguous int32 [B] tensor on the cache's device")
+
+
+def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], call):
+    """call(stream handle) with `dev` current, and `stream`, where given, the current stream too, so that what the call
+    allocates belongs to the stream that uses it."""
+    if stream is None and torch.cuda.current_device() == dev.index:  # nothing to change, as in a decode loop
+        return call(_raw_stream(dev.index))
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return call(_raw_stream(dev.index) if stream is None else stream.cuda_stream)
+
+
+def _raw_stream(index: int) -> int:
+    """The handle of the device's current stream."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (without making a Stream object)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def kvq_write(cache, k: torch.Tensor, v: torch.Tensor, cache_seqlens: torch.Tensor,
@@ -409,10 +432,8 @@ def kvq_write(cache, k: torch.Tensor, v: torch.Tensor, cache_seqlens: torch.Tens
         raise ValueError(f"k has shape {tuple(k.shape)}; expected [{B}, T, {Hkv}, {D}]")
     _check_qkv("v", v, k.shape, dev)
     _check_seqlens(cache_seqlens, B, dev)
-    with torch.cuda.device(dev):
-        st = lib.attn_kvq_write(k.data_ptr(), v.data_ptr(), *ptrs, cache_seqlens.data_ptr(), B, T, Hkv, Tk, D, bits,
-                                group, _stream_handle(stream, dev))
-    _check("attn_kvq_write", st)
+    _check("attn_kvq_write", _launch(dev, stream, lambda handle: lib.attn_kvq_write(
+        k.data_ptr(), v.data_ptr(), *ptrs, cache_seqlens.data_ptr(), B, T, Hkv, Tk, D, bits, group, handle)))
 
 
 def kvq_read(cache, T: Optional[int] = None, cache_seqlens: Optional[torch.Tensor] = None,
@@ -430,16 +451,25 @@ def kvq_read(cache, T: Optional[int] = None, cache_seqlens: Optional[torch.Tenso
     if cache_seqlens is not None:
         _check_seqlens(cache_seqlens, B, dev)
     shape = (B, T, Hkv, 128)
-    # outputs made here belong to the stream that fills them
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-        _check_qkv("k", k, shape, dev)
-        _check_qkv("v", v, shape, dev)
-        st = lib.attn_kvq_read(*ptrs, None if cache_seqlens is None else cache_seqlens.data_ptr(), k.data_ptr(),
-                               v.data_ptr(), B, T, Hkv, Tk, 128, bits, group, _stream_handle(stream, dev))
-    _check("attn_kvq_read", st)
-    return k, v
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _check_qkv(name, t, shape, dev)
+    out_k, out_v = k, v
+
+    def call(handle):
+        nonlocal out_k, out_v
+        out_k = cache[1].new_empty(shape) if out_k is None else out_k
+        out_v = cache[1].new_empty(shape) if out_v is None else out_v
+        return lib.attn_kvq_read(*ptrs, None if cache_seqlens is None else cache_seqlens.data_ptr(), out_k.data_ptr(),
+                                 out_v.data_ptr(), B, T, Hkv, Tk, 128, bits, group, handle)
+
+    _check("attn_kvq_read", _launch(dev, stream, call))
+    return out_k, out_v
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_kvq_workspace(B: int, H: int, Hkv: int, Tq: int, Tk: int, D: int) -> int:
+    return max(int(load_library().attn_decode_kvq_workspace_bytes(B, H, Hkv, Tq, Tk, D)), 16)
 
 
 def attn_decode_kvq(q: torch.Tensor, cache, cache_seqlens: torch.Tensor, scale: Optional[float] = None,
@@ -461,23 +491,27 @@ def attn_decode_kvq(q: torch.Tensor, cache, cache_seqlens: torch.Tensor, scale: 
     _check_seqlens(cache_seqlens, B, dev)
     scale = default_scale(D) if scale is None else float(scale)
     win = _window_arg(window)
-    # outputs and workspace made here belong to the stream that uses them
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        o = torch.empty_like(q) if o is None else o
+    if o is not None:
         _check_qkv("o", o, q.shape, dev)
-        if lse is None:
-            lse = torch.empty((B, H, Tq), dtype=torch.float32, device=dev)
+    if lse is not None:
         _check_f32("lse", lse, (B, H, Tq), dev)
-        if workspace is None:
-            workspace = torch.empty(max(int(lib.attn_decode_kvq_workspace_bytes(B, H, Hkv, Tq, Tk, D)), 16),
-                                    dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {dev}, like every tensor of one call")
-        st = lib.attn_decode_kvq(q.data_ptr(), *ptrs, cache_seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, H, Hkv, Tq,
-                                 Tk, D, bits, group, scale, win, _stream_handle(stream, dev))
-    _check("attn_decode_kvq", st)
-    return o, lse
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous and on {dev}, like every tensor of one call")
+    out, out_lse = o, lse
+
+    def call(handle):
+        nonlocal out, out_lse
+        out = torch.empty_like(q) if out is None else out
+        out_lse = q.new_empty((B, H, Tq), dtype=torch.float32) if out_lse is None else out_lse
+        ws = workspace
+        if ws is None:
+            ws = q.new_empty(_decode_kvq_workspace(B, H, Hkv, Tq, Tk, D), dtype=torch.uint8)
+        return lib.attn_decode_kvq(q.data_ptr(), *ptrs, cache_seqlens.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
+                                   ws.data_ptr(), ws.numel() * ws.element_size(), B, H, Hkv, Tq, Tk, D, bits, group,
+                                   scale, win, handle)
+
+    _check("attn_decode_kvq", _launch(dev, stream, call))
+    return out, out_lse
 
 
 ROPE_PAIRINGS = {"interleaved": 0, "half": 1}

@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -376,15 +377,31 @@ int decode_span(int Tq, int Tk, int window) {
   return window < 0 ? Tk : static_cast<int>(std::min<long long>(Tk, static_cast<long long>(Tq) + window));
 }
 
-// CTAs of the split kernel: one per SM, or fewer where every warp of a CTA would not get a 16-key tile.
-unsigned decode_grid(int B, int H, int Hkv, int Tq, int span) {
+// How a decode call is split: the split kernel's CTAs, one per SM or fewer where there is not a 16-key tile for every warp,
+// and whether each of them has whole units. That spares the merge kernel (2 to 3 us of a call) but leaves the CTAs uneven,
+// so it is for small calls: a warp has four 16-key tiles at most. (With one sequence of 4 x 192 keys and 2 to 148 units
+// the calls took 9 to 11 us in whole units and 10 to 13 us without.)
+struct DecodeSplit {
+  unsigned ctas;
+  bool whole;
+};
+DecodeSplit decode_split(int B, int H, int Hkv, int Tq, int span) {
   const int R = (H / Hkv) * Tq, n_rt = (R + 7) / 8, slices = attn::kKvqWarps / n_rt;
-  const long long tiles = static_cast<long long>(B) * Hkv * ((span + 15) / 16);
-  return static_cast<unsigned>(std::min<long long>(attn::kKvqCtas, (tiles + slices - 1) / slices));
+  const long long units = static_cast<long long>(B) * Hkv, each = (span + 15) / 16;
+  const long long per_cta = (units + attn::kKvqCtas - 1) / attn::kKvqCtas;
+  if (per_cta * each <= 4 * slices && per_cta <= 32)
+    return {static_cast<unsigned>(std::min<long long>(attn::kKvqCtas, units)), true};
+  return {static_cast<unsigned>(std::min<long long>(attn::kKvqCtas, (units * each + slices - 1) / slices)), false};
 }
 
+// Room for the pieces of the most CTAs that any window makes (fewer keys are never split over more of them).
+size_t decode_pieces(int B, int H, int Hkv, int Tq, int Tk) {
+  const int R = (H / Hkv) * Tq, slices = attn::kKvqWarps / ((R + 7) / 8);
+  const long long tiles = static_cast<long long>(B) * Hkv * ((Tk + 15) / 16);
+  return static_cast<size_t>(std::min<long long>(attn::kKvqCtas, (tiles + slices - 1) / slices));
+}
 size_t decode_workspace(int B, int H, int Hkv, int Tq, int Tk) {
-  const size_t pieces = static_cast<size_t>(decode_grid(B, H, Hkv, Tq, Tk)), rows = pieces * 2 * ((H / Hkv) * Tq);
+  const size_t pieces = decode_pieces(B, H, Hkv, Tq, Tk), rows = pieces * 2 * ((H / Hkv) * Tq);
   return pieces * sizeof(attn::KvqSpan) + rows * (128 + 2) * 4;
 }
 
@@ -393,8 +410,15 @@ cudaError_t launch_split(const attn::KvqDecodeParams& p, unsigned ctas, cudaStre
   auto kernel = attn::kvq_decode_split_kernel<kBits, kGroup>;
   constexpr int kSmem = attn::KvqShape<kBits, kGroup>::kSmem;
   static_assert(kSmem + 1024 <= 227 * 1024, "one CTA per SM");
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> done{0};  // devices (by number, below 64) whose opt-in is made
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
   return launch_early(kernel, dim3(ctas), attn::kKvqThreads, kSmem, s, p);
 }
 
@@ -467,7 +491,8 @@ size_t attn_decode_kvq_workspace_bytes(int B, int H, int H_kv, int Tq, int Tk, i
 
 int attn_decode_kvq_kernels(int B, int H, int H_kv, int Tq, int Tk, int D, int window) {
   if (check_decode(B, H, H_kv, Tq, Tk, D, 4, 128, 1.0f) != ATTN_OK || window < -1) return 0;
-  return decode_grid(B, H, H_kv, Tq, decode_span(Tq, Tk, window)) > 1 ? 2 : 1;
+  const DecodeSplit split = decode_split(B, H, H_kv, Tq, decode_span(Tq, Tk, window));
+  return split.whole || split.ctas == 1 ? 1 : 2;
 }
 
 attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
@@ -505,9 +530,10 @@ attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_pa
   p.scale_log2 = scale * 1.4426950408889634f;
   const int R = p.R = (H / H_kv) * Tq;
   for (int r = 0; r < attn::kKvqMaxRows; ++r) p.row_i[r] = r < R ? r % Tq : 0, p.row_g[r] = r < R ? r / Tq : 0;
-  const unsigned ctas = decode_grid(B, H, H_kv, Tq, decode_span(Tq, Tk, window));
-  // (laid out for the most CTAs, those without a window)
-  const size_t most = decode_grid(B, H, H_kv, Tq, Tk);
+  const DecodeSplit split = decode_split(B, H, H_kv, Tq, decode_span(Tq, Tk, window));
+  const unsigned ctas = split.ctas;
+  p.whole = split.whole;
+  const size_t most = decode_pieces(B, H, H_kv, Tq, Tk);
   p.spans = static_cast<attn::KvqSpan*>(workspace);
   p.part_o = reinterpret_cast<float*>(p.spans + most);
   p.part_ml = p.part_o + most * 2 * R * 128;
@@ -517,7 +543,7 @@ attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_pa
     e = launch_split<b.value, g.value>(p, ctas, s);
   });
   if (e != cudaSuccess) return cuda_fail(e, "kvq_decode_split_kernel launch");
-  if (ctas > 1) {
+  if (!split.whole && ctas > 1) {
     // A unit spans about ctas / (B * H_kv) CTAs: with many pieces to a unit a block takes one row, with few up to 8.
     if (R == 1 || static_cast<long long>(B) * H_kv * 8 < ctas)
       e = launch_early(attn::kvq_decode_merge_kernel<1>, dim3(ctas, R), 256, 0, s, p);

@@ -88,6 +88,7 @@ struct KvqDecodeParams {
   float* part_o;                 // [grid, 2, R, 128]: its unnormalised output
   int B, H, Hkv, Tq, Tk, R;
   int window;                    // sliding window: the query at position p sees keys p - window .. p; -1: none
+  int whole;                     // 1: every CTA has whole units (at most 32 of them): no piece is left to merge
   float scale_log2;              // scale * log2(e)
   uint8_t row_i[kKvqMaxRows], row_g[kKvqMaxRows];  // row r is token r % Tq of query head r / Tq of the group
 };
@@ -289,36 +290,41 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   const int slices = kKvqWarps / n_rt;  // stretches per CTA, each for the n_rt warps of its row tiles
   const int rt = warp % n_rt, slice = warp / n_rt;
   if (rt == 0 && lane < 2) sh_piece[2 * slice + lane].unit = -1;  // (this warp's to write; read after the barrier)
-  if (tid == 0) p.spans[blockIdx.x].unit = -1;
+  if (tid == 0 && !p.whole) p.spans[blockIdx.x].unit = -1;
 
-  // Every warp looks for itself where its stretch of the row of all places begins, 32 sequences at a time. A sequence
-  // without tiles has no places; otherwise each of its units has kKvqUnitCost places, then its tiles'.
-  auto places = [&](int b) {
-    const int n = b < p.B ? kvq_seq<kTile>(p, b).tiles : 0;
-    return n ? (n + kKvqUnitCost) * p.Hkv : 0;
+  // Every warp looks for itself where its stretch of the row of all places begins, 32 items at a time. An item is a
+  // sequence with its H_kv units, or with p.whole one of the units that this CTA has to itself (the row is then the
+  // CTA's). A unit without tiles has no places; otherwise it has kKvqUnitCost, then its tiles'.
+  const int n_units = p.B * p.Hkv;
+  const int u0 = p.whole ? static_cast<int>(static_cast<long long>(blockIdx.x) * n_units / gridDim.x) : 0;
+  const int u1 = p.whole ? static_cast<int>(static_cast<long long>(blockIdx.x + 1) * n_units / gridDim.x) : n_units;
+  const int each_item = p.whole ? 1 : p.Hkv, items = p.whole ? u1 - u0 : p.B;
+  auto places = [&](int i) {
+    const int n = i < items ? kvq_seq<kTile>(p, p.whole ? (u0 + i) / p.Hkv : i).tiles : 0;
+    return n ? (n + kKvqUnitCost) * each_item : 0;
   };
   int total = 0;
-  bool empty = false;  // whether there are sequences without keys
-  for (int b = lane; b < p.B; b += 32) {
-    const int n = places(b);
+  bool empty = p.whole;  // whether there may be sequences without keys
+  for (int i = lane; i < items; i += 32) {
+    const int n = places(i);
     total += n;
     empty |= n == 0;
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  const int stretches = static_cast<int>(gridDim.x) * slices;
+  const int stretches = (p.whole ? 1 : static_cast<int>(gridDim.x)) * slices, stretch0 = p.whole ? 0 : blockIdx.x * slices;
   int share = static_cast<int>(ceilf(static_cast<float>(total) * __frcp_rn(static_cast<float>(stretches))));
   while (static_cast<long long>(share) * stretches < total) ++share;  // (where fp32 is too coarse)
   // Stretch i of this CTA is places [start_of(i), start_of(i + 1)); its tiles are those whose places it has.
   auto start_of = [&](int i) {
-    return static_cast<int>(min(static_cast<long long>(total), (static_cast<long long>(blockIdx.x) * slices + i) * share));
+    return static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(stretch0 + i) * share));
   };
   const int first = start_of(slice), last = start_of(slice + 1);
   KvqCursor cur = {};  // the unit being computed, from its tile cur.tile on
   cur.end = total;
   if (first < last) {
-    for (int b0 = 0, before = 0;; b0 += 32) {
-      const int n = places(b0 + lane);
+    for (int i0 = 0, before = 0;; i0 += 32) {
+      const int n = places(i0 + lane);
       int incl = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -326,13 +332,13 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         if (lane >= d) incl += y;
       }
       const unsigned past = __ballot_sync(0xffffffffu, before + incl > first);
-      if (past) {  // (some sequence ends past it: first < total)
+      if (past) {  // (some item ends past it: first < total)
         const int l = __ffs(past) - 1, start = before + __shfl_sync(0xffffffffu, incl - n, l);
-        cur.b = b0 + l;
+        cur.b = p.whole ? (u0 + l) / p.Hkv : i0 + l;
         cur.s = kvq_seq<kTile>(p, cur.b);
-        const int each = cur.s.tiles + kKvqUnitCost;
-        cur.hk = (first - start) / each;
-        cur.end = start + (cur.hk + 1) * each;
+        const int each = cur.s.tiles + kKvqUnitCost, at = (first - start) / each;
+        cur.hk = p.whole ? u0 + l - cur.b * p.Hkv : at;
+        cur.end = start + (at + 1) * each;
         cur.tile = max(first - (cur.end - cur.s.tiles), 0);
         break;
       }
