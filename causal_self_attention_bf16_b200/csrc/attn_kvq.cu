@@ -378,9 +378,11 @@ int decode_span(int Tq, int Tk, int window) {
 }
 
 // How a decode call is split: the split kernel's CTAs, one per SM or fewer where there is not a 16-key tile for every warp,
-// and whether each of them has whole units. That spares the merge kernel (2 to 3 us of a call) but leaves the CTAs uneven,
-// so it is for small calls: a warp has four 16-key tiles at most. (With one sequence of 4 x 192 keys and 2 to 148 units
-// the calls took 9 to 11 us in whole units and 10 to 13 us without.)
+// and whether each of them has whole units. That spares the merge kernel but leaves CTAs uneven, or idle where there are
+// fewer units, so it is for small calls: up to 8 tiles of 16 keys a warp where there are units for (nearly) all CTAs, else
+// up to 4. Measured, whole / split: 640 units of 200 keys 11.4 / 13.8 us, of 1 to 200 keys 11.8 / 12.6; 140 units of 192
+// keys 6.9 / 9.2, of 1,500 keys 12.6 / 13.8, of 1 to 2,000 keys (over the limit) 14.2 / 12.4; 10 units of 384 keys
+// 7.3 / 8.8, of 1,500 keys (over it) 12.0 / 9.1.
 struct DecodeSplit {
   unsigned ctas;
   bool whole;
@@ -389,7 +391,7 @@ DecodeSplit decode_split(int B, int H, int Hkv, int Tq, int span) {
   const int R = (H / Hkv) * Tq, n_rt = (R + 7) / 8, slices = attn::kKvqWarps / n_rt;
   const long long units = static_cast<long long>(B) * Hkv, each = (span + 15) / 16;
   const long long per_cta = (units + attn::kKvqCtas - 1) / attn::kKvqCtas;
-  if (per_cta * each <= 4 * slices && per_cta <= 32)
+  if (per_cta * each <= (4 * units >= 3 * attn::kKvqCtas ? 8 : 4) * slices && per_cta <= 32)
     return {static_cast<unsigned>(std::min<long long>(attn::kKvqCtas, units)), true};
   return {static_cast<unsigned>(std::min<long long>(attn::kKvqCtas, (units * each + slices - 1) / slices)), false};
 }
