@@ -382,8 +382,10 @@ def _check_kvq(cache):
     dev, cs, ps = kc.device, kc.shape, kp.shape
     if len(cs) != 4 or cs[3] not in (64, 128) or 0 in cs:
         raise ValueError(f"k_codes has shape {tuple(cs)}; expected [B, H_kv, Tk, 64] (4 bits) or [.., 128] (8 bits)")
-    if len(ps) != 5 or ps[:3] != cs[:3] or ps[3] not in (1, 2, 4) or ps[4] != 2:
-        raise ValueError(f"k_params has shape {tuple(ps)}; expected [{cs[0]}, {cs[1]}, {cs[2]}, 128 // group, 2]")
+    B, Hkv, Tk, row = cs
+    groups = ps[3] if len(ps) == 5 else 0
+    if groups not in (1, 2, 4) or ps != (B, Hkv, Tk, groups, 2):
+        raise ValueError(f"k_params has shape {tuple(ps)}; expected [{B}, {Hkv}, {Tk}, 128 // group, 2]")
     if not (kc.dtype == vc.dtype == torch.uint8 and kp.dtype == vp.dtype == torch.bfloat16 and vc.shape == cs
             and vp.shape == ps and kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous()
             and vp.is_contiguous() and kp.device == dev and vc.device == dev and vp.device == dev):
@@ -393,8 +395,7 @@ def _check_kvq(cache):
                 raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor")
             if t.device != dev:
                 raise ValueError(f"{name} is on {t.device}; every tensor of one call must be on {dev}")
-    return ((kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), cs[0], cs[1], cs[2], cs[3] // 16,
-            128 // ps[3], dev)
+    return (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), B, Hkv, Tk, row // 16, 128 // groups, dev
 
 
 def _check_seqlens(cache_seqlens, B: int, dev: torch.device):
@@ -469,7 +470,7 @@ def kvq_read(cache, T: Optional[int] = None, cache_seqlens: Optional[torch.Tenso
 
 @functools.lru_cache(maxsize=1024)
 def _decode_kvq_workspace(B: int, H: int, Hkv: int, Tq: int, Tk: int, D: int) -> int:
-    return max(int(load_library().attn_decode_kvq_workspace_bytes(B, H, Hkv, Tq, Tk, D)), 16)
+    return int(load_library().attn_decode_kvq_workspace_bytes(B, H, Hkv, Tq, Tk, D))
 
 
 def attn_decode_kvq(q: torch.Tensor, cache, cache_seqlens: torch.Tensor, scale: Optional[float] = None,
@@ -505,10 +506,11 @@ def attn_decode_kvq(q: torch.Tensor, cache, cache_seqlens: torch.Tensor, scale: 
         out_lse = q.new_empty((B, H, Tq), dtype=torch.float32) if out_lse is None else out_lse
         ws = workspace
         if ws is None:
-            ws = q.new_empty(_decode_kvq_workspace(B, H, Hkv, Tq, Tk, D), dtype=torch.uint8)
+            need = _decode_kvq_workspace(B, H, Hkv, Tq, Tk, D)
+            ws = q.new_empty(need, dtype=torch.uint8) if need else None
+        ws_ptr, ws_bytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
         return lib.attn_decode_kvq(q.data_ptr(), *ptrs, cache_seqlens.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
-                                   ws.data_ptr(), ws.numel() * ws.element_size(), B, H, Hkv, Tq, Tk, D, bits, group,
-                                   scale, win, handle)
+                                   ws_ptr, ws_bytes, B, H, Hkv, Tq, Tk, D, bits, group, scale, win, handle)
 
     _check("attn_decode_kvq", _launch(dev, stream, call))
     return out, out_lse

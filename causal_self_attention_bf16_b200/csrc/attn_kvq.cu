@@ -403,6 +403,7 @@ size_t decode_pieces(int B, int H, int Hkv, int Tq, int Tk) {
   return static_cast<size_t>(std::min<long long>(attn::kKvqCtas, (tiles + slices - 1) / slices));
 }
 size_t decode_workspace(int B, int H, int Hkv, int Tq, int Tk) {
+  if (decode_split(B, H, Hkv, Tq, Tk).whole) return 0;  // (and so with any window, which only leaves fewer keys)
   const size_t pieces = decode_pieces(B, H, Hkv, Tq, Tk), rows = pieces * 2 * ((H / Hkv) * Tq);
   return pieces * sizeof(attn::KvqSpan) + rows * (128 + 2) * 4;
 }
@@ -507,7 +508,7 @@ attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_pa
   if (st != ATTN_OK) return st;
   if (window < -1) return ATTN_ERR_INVALID_ARG;
   const size_t need = attn_decode_kvq_workspace_bytes(B, H, H_kv, Tq, Tk, D);
-  if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+  if (need && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
   for (const void* ptr : {q, k_codes, k_params, v_codes, v_params, static_cast<const void*>(o),
                           static_cast<const void*>(workspace)})
     if (!aligned(ptr, 16)) return ATTN_ERR_MISALIGNED;

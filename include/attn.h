@@ -281,8 +281,10 @@ attn_status attn_kvq_read(const void* k_codes, const void* k_params, const void*
  *   hold. A NaN in a key that a query sees makes that query's o and lse NaN, one in a value its o, in the group's dims.
  *   workspace scratch : attn_decode_kvq_workspace_bytes(B, H, H_kv, Tq, Tk, D) bytes, 16-byte aligned, for any
  *   window, bits and group; its contents on entry do not matter. Calls sharing a workspace must not overlap in time
- *   on the GPU.
- * attn_decode_kvq_kernels: the kernels one call launches (0 for arguments the call rejects). Host-only.
+ *   on the GPU. 0 bytes for small calls, which may pass NULL (the query also returns 0 for arguments the call rejects).
+ * attn_decode_kvq_kernels: the kernels one call launches, 1 or 2 (0 for arguments the call rejects). Host-only.
+ * The three calls' kernels start up while the one before them on the stream still runs and wait for its end before they
+ * read or write anything (programmatic dependent launch), so the usual stream order holds.
  */
 size_t attn_decode_kvq_workspace_bytes(int B, int H, int H_kv, int Tq, int Tk, int D);
 int attn_decode_kvq_kernels(int B, int H, int H_kv, int Tq, int Tk, int D, int window);
