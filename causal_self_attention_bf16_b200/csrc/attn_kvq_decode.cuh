@@ -488,13 +488,13 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
           for (int y = 0; y < 4; ++y) qb[4 * x + y] = f[y];
         }
-        // the sums of q over a group's dims: products with 2^-24 everywhere (2^-20 for the numbers that are 2^4 smaller)
-        constexpr uint32_t kOne = 0x00010001u, kSecond = kBits == 4 ? 0x00100010u : kOne;
+        // the sums of q over a group's dims: products with 1 (16 for the numbers that are 2^4 smaller)
+        constexpr uint32_t kOne = 0x3c003c00u, kSecond = kBits == 4 ? 0x4c004c00u : kOne;
         const int j = x / (kGroup / 32);
         if (x % (kGroup / 32) == 0) mma_16x8x16_first(qs[j], kOne, kOne, kSecond, kSecond, qb[4 * x], qb[4 * x + 1]);
         else mma_16x8x16(qs[j], kOne, kOne, kSecond, kSecond, qb[4 * x], qb[4 * x + 1]);
         mma_16x8x16(qs[j], kOne, kOne, kSecond, kSecond, qb[4 * x + 2], qb[4 * x + 3]);
-        qsum[j][0] = qs[j][0], qsum[j][1] = qs[j][1];
+        qsum[j][0] = qs[j][0] * 0x1p-24f, qsum[j][1] = qs[j][1] * 0x1p-24f;
       }
       const float back = (p.scale_log2 * 0x1p24f) * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
       down[0] = __shfl_sync(0xffffffffu, back, 8 * t);
