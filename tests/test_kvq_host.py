@@ -169,7 +169,32 @@ def test_decode_sizes_refused_by_the_host_queries(lib):
     ws, kern = lib.attn_decode_kvq_workspace_bytes, lib.attn_decode_kvq_kernels
     assert ws(2, 8, 3, 1, 1000, 128) == 0 and ws(2, 64, 1, 1, 1000, 128) == 0 and ws(0, 8, 2, 1, 10, 128) == 0
     assert kern(2, 8, 3, 1, 1000, 128, -1) == 0 and kern(2, 8, 2, 1, 1000, 128, -2) == 0
-    assert kern(2, 8, 2, 1, 1000, 128, -1) >= 1
+
+
+def test_decode_split_rule(lib):
+    """Small calls are whole units, one kernel without a workspace: up to 8 tiles of 16 keys for each of a CTA's 12 warps
+    where the units fill three quarters of 148 CTAs, else 4 (the warps shared by the row tiles of 8 query rows). Others
+    are split over up to 148 CTAs: a span (16 bytes) per CTA, and two pieces of 130 floats per CTA and row."""
+    ws, kern = lib.attn_decode_kvq_workspace_bytes, lib.attn_decode_kvq_kernels
+    for B, H, hkv, Tq, Tk, whole in ((3, 4, 2, 2, 300, True),      # 6 units of 19 tiles
+                                     (1, 10, 10, 1, 768, True),    # 10 units of 48 tiles: 4 a warp
+                                     (1, 10, 10, 1, 769, False),
+                                     (14, 10, 10, 1, 1536, True),  # 140 units of 96 tiles: 8 a warp
+                                     (14, 10, 10, 1, 1537, False),
+                                     (64, 10, 10, 1, 300, True),   # 5 units to a CTA, 19 tiles each
+                                     (64, 10, 10, 1, 320, False),  # 20 tiles each
+                                     (16, 12, 3, 8, 128, True),    # 32 rows: three stretches of 8 tiles
+                                     (16, 12, 3, 8, 193, False),
+                                     (5000, 1, 1, 1, 16, False)):  # 34 units to a CTA: more than its warps look at
+        assert kern(B, H, hkv, Tq, Tk, 128, -1) == (1 if whole else 2), (B, H, hkv, Tq, Tk)
+        if whole:
+            assert ws(B, H, hkv, Tq, Tk, 128) == 0
+        else:
+            R = H // hkv * Tq
+            slices = 12 // ((R + 7) // 8)
+            ctas = min(148, (B * hkv * ((Tk + 15) // 16) + slices - 1) // slices)
+            assert ws(B, H, hkv, Tq, Tk, 128) == ctas * 16 + ctas * 2 * R * 130 * 4
+    assert kern(64, 10, 10, 1, 2048, 128, -1) == 2 and kern(64, 10, 10, 1, 2048, 128, 300) == 1  # a window's few keys
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU behaviour")

@@ -273,7 +273,7 @@ def test_decode_every_row_count(R, bits):
     run_decode(2, R, 1, 1, 200, bits, 64, [200, 33], seed=R)
 
 
-@pytest.mark.parametrize("window", [0, 1, 15, 16, 100, 700, 5000])
+@pytest.mark.parametrize("window", [0, 1, 15, 16, 100, 699, 700, 5000, 2 ** 31 - 1])
 @pytest.mark.parametrize("bits,group", [(4, 64), (8, 32)])
 def test_decode_window(window, bits, group):
     run_decode(3, 4, 2, 3, 700, bits, group, [700, 2, 333], window=window)
@@ -295,6 +295,81 @@ def test_decode_ragged_batch():
     """Many sequences of very different lengths: each must be seen whole, once."""
     lens = [(37 * i * i) % 501 for i in range(60)]
     run_decode(60, 2, 2, 1, 500, 4, 64, lens)
+
+
+@pytest.mark.parametrize("bits,group,Tk", [(4, 64, 20), (4, 32, 70), (8, 128, 33), (8, 64, 700)])
+def test_decode_many_short_sequences(bits, group, Tk):
+    """Hundreds of sequences of 0 to Tk keys: several units to a warp, and sequences without keys between them."""
+    lens = [(13 * i * i + i) % (Tk + 1) if i % 7 else 0 for i in range(400)]
+    run_decode(400, 2, 1, 1, Tk, bits, group, lens)
+
+
+@pytest.mark.parametrize("Tk", [768, 769])
+@pytest.mark.parametrize("H,Tq", [(1, 1), (3, 4), (8, 4)])
+def test_decode_on_both_sides_of_the_split_rule(Tk, H, Tq):
+    """The same keys in whole units and split over CTAs (a capacity past the rule's limit): the oracle's result, and each
+    other's up to the rounding of the joined sums."""
+    lens = [700, 31]
+    q, cache, o, lse = run_decode(2, H, 1, Tq, Tk, 4, 64, lens)
+    wide = attn.kvq_cache(2, 1, 4000, 4, 64)
+    for a, b in zip(wide, cache):
+        a[:, :, :Tk] = b
+    o2, lse2 = attn.attn_decode_kvq(q, wide, ints(lens))
+    clean()
+    check_decode(q, wide, lens, 128 ** -0.5, None, o2, lse2, "wide")
+    assert torch.allclose(lse, lse2, rtol=2 ** -20, atol=2 ** -18)
+
+
+@pytest.mark.parametrize("T", [1, 3, 64])
+def test_more_tokens_than_keys(T):
+    """Sequences shorter than the call's tokens, through all three calls."""
+    B, Hkv = 3, 2
+    lens = [2, 0, 1]
+    cache = poisoned(B, Hkv, 5, 8, 32)
+    k, v = randn((B, T, Hkv, 128), 200).cuda(), randn((B, T, Hkv, 128), 201).cuda()
+    attn.kvq_write(cache, k, v, ints(lens))
+    rk, rv = attn.kvq_read(cache, T, ints(lens))
+    q = randn((B, min(T, 32), Hkv, 128), 202).cuda()
+    o, lse = attn.attn_decode_kvq(q, cache, ints([min(L, T) for L in lens]))
+    clean()
+    for b, L in enumerate(lens):
+        n = min(L, T)
+        assert (rk[b, :T - n] == 0).all() and (rv[b, :T - n] == 0).all()
+        check_row(k[b, T - n:].cpu(), cache.k_codes[b, :, L - n:L].transpose(0, 1),
+                  cache.k_params[b, :, L - n:L].transpose(0, 1), 8, 32, "k")
+    if T > 1:  # (with one token only sequence 0's second key is written: its first row is still NaN)
+        check_decode(q, cache, lens, 128 ** -0.5, None, o, lse, "short")
+    assert (o[1] == 0).all() and (lse[1] == -float("inf")).all()
+
+
+def test_refusals_on_the_device():
+    """What the binding refuses with CUDA tensors in hand; nothing is launched and the cache stays."""
+    cache = attn.kvq_cache(2, 3, 8)
+    before = [t.clone() for t in cache]
+    k = torch.ones(2, 4, 3, 128, dtype=torch.bfloat16, device="cuda")
+    q = torch.ones(2, 1, 6, 128, dtype=torch.bfloat16, device="cuda")
+    lens = ints([4, 4])
+    for call in (lambda: attn.kvq_write(cache, k.half(), k, lens), lambda: attn.kvq_write(cache, k, k[:, :3], lens),
+                 lambda: attn.kvq_write(cache, k[:, :, :2].contiguous(), k[:, :, :2].contiguous(), lens),
+                 lambda: attn.kvq_write(cache, k[:1], k[:1], lens), lambda: attn.kvq_write(cache, k, k, lens.long()),
+                 lambda: attn.kvq_write(cache, k, k, lens.cpu()), lambda: attn.kvq_write(cache, k.transpose(1, 2), k, lens),
+                 lambda: attn.kvq_read(cache, 0), lambda: attn.kvq_read(cache, 9), lambda: attn.kvq_read(cache, 4, lens[:1]),
+                 lambda: attn.kvq_read(cache, 4, lens, k.float(), k), lambda: attn.kvq_read(cache, 4, lens, k[:, :3], k),
+                 lambda: attn.attn_decode_kvq(q.float(), cache, lens), lambda: attn.attn_decode_kvq(q[:1], cache, lens),
+                 lambda: attn.attn_decode_kvq(q, cache, lens, window=-1),
+                 lambda: attn.attn_decode_kvq(q, cache, lens, o=q[:, :, :3]),
+                 lambda: attn.attn_decode_kvq(q, cache, lens, lse=torch.empty(2, 6, 2, device="cuda")),
+                 lambda: attn.attn_decode_kvq(q, cache, lens, workspace=torch.empty(64))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: attn.attn_decode_kvq(q[:, :, :5].contiguous(), cache, lens),             # 5 heads over 3
+                 lambda: attn.attn_decode_kvq(q.repeat(1, 17, 1, 1), cache, lens),                # 34 rows
+                 lambda: attn.attn_decode_kvq(q, cache, lens, 0.0), lambda: attn.attn_decode_kvq(q, cache, lens, o=q),
+                 lambda: attn.kvq_read(cache, 4, lens, k, k)):                                    # one output twice
+        with pytest.raises(attn.AttnError):
+            call()
+    clean()
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(cache, before))
 
 
 def test_decode_large_scores():
