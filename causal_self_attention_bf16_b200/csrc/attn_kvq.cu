@@ -536,6 +536,7 @@ attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_pa
   const DecodeSplit split = decode_split(B, H, H_kv, Tq, decode_span(Tq, Tk, window));
   const unsigned ctas = split.ctas;
   p.whole = split.whole;
+  p.per_stretch = 1.0 / ((split.whole ? 1.0 : ctas) * (attn::kKvqWarps / ((R + 7) / 8)));
   const size_t most = decode_pieces(B, H, H_kv, Tq, Tk);
   p.spans = static_cast<attn::KvqSpan*>(workspace);
   p.part_o = reinterpret_cast<float*>(p.spans + most);

@@ -90,6 +90,7 @@ struct KvqDecodeParams {
   int window;                    // sliding window: the query at position p sees keys p - window .. p; -1: none
   int whole;                     // 1: every CTA has whole units (at most 32 of them): no piece is left to merge
   float scale_log2;              // scale * log2(e)
+  double per_stretch;            // 1 / the warps' stretches of the row of all places (of the CTA's with `whole`)
   uint8_t row_i[kKvqMaxRows], row_g[kKvqMaxRows];  // row r is token r % Tq of query head r / Tq of the group
 };
 
@@ -313,12 +314,14 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
   for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
   const int stretches = (p.whole ? 1 : static_cast<int>(gridDim.x)) * slices, stretch0 = p.whole ? 0 : blockIdx.x * slices;
-  int share = static_cast<int>(ceilf(static_cast<float>(total) * __frcp_rn(static_cast<float>(stretches))));
-  while (static_cast<long long>(share) * stretches < total) ++share;  // (where fp32 is too coarse)
-  // Stretch i of this CTA is places [start_of(i), start_of(i + 1)); its tiles are those whose places it has.
-  auto start_of = [&](int i) {
-    return static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(stretch0 + i) * share));
+  // Stretch i of all begins at place i * total / stretches, rounded down (the half place keeps the product's rounding away
+  // from whole numbers), so that every CTA has the same number of places, to one; with fewer places than stretches the
+  // first ones have one each. No stretch before another's end is empty. A stretch's tiles are those whose places it has.
+  auto begin_of = [&](int i) {
+    if (total <= stretches || i >= stretches) return min(i < stretches ? i : total, total);
+    return static_cast<int>((static_cast<double>(static_cast<long long>(i) * total) + 0.5) * p.per_stretch);
   };
+  auto start_of = [&](int i) { return begin_of(stretch0 + i); };  // the CTA's i-th
   const int first = start_of(slice), last = start_of(slice + 1);
   KvqCursor cur = {};  // the unit being computed, from its tile cur.tile on
   cur.end = total;
@@ -806,7 +809,13 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
           if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(M, L);
         }
         if (r == 0 && lane == 0 && begins)  // it begins here and goes on past this CTA
-          p.spans[blockIdx.x] = KvqSpan{unit, (end - 1) / (share * slices), slot, 0};
+        {
+          int c = min(static_cast<int>(static_cast<double>(end - 1) / (static_cast<double>(total) * p.per_stretch)) / slices,
+                      static_cast<int>(gridDim.x) - 1);  // the CTA of its last place
+          while (c > 0 && begin_of(c * slices) >= end) --c;
+          while (begin_of((c + 1) * slices) < end) ++c;
+          p.spans[blockIdx.x] = KvqSpan{unit, c, slot, 0};
+        }
       }
     }
   }
