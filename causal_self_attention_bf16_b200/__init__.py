@@ -398,6 +398,11 @@ def _check_kvq(cache):
     return (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), B, Hkv, Tk, row // 16, 128 // groups, dev
 
 
+def _require_cuda_cache(dev: torch.device) -> None:
+    if dev.type != "cuda":
+        raise ValueError("the cache's tensors must be CUDA tensors")
+
+
 def _check_seqlens(cache_seqlens, B: int, dev: torch.device):
     if (not isinstance(cache_seqlens, torch.Tensor) or cache_seqlens.dtype != torch.int32 or
             cache_seqlens.shape != (B,) or cache_seqlens.device != dev or not cache_seqlens.is_contiguous()):
@@ -426,7 +431,7 @@ def kvq_write(cache, k: torch.Tensor, v: torch.Tensor, cache_seqlens: torch.Tens
     sequence b is written at position cache_seqlens[b] - T + i, or not at all where that is below 0."""
     lib = load_library()
     ptrs, B, Hkv, Tk, bits, group, dev = _check_kvq(cache)
-    _require_cuda("k_codes", cache[0])
+    _require_cuda_cache(dev)
     _check_qkv("k", k, device=dev)
     T, D = k.shape[1], k.shape[3]
     if (k.shape[0], k.shape[2]) != (B, Hkv):
@@ -445,7 +450,7 @@ def kvq_read(cache, T: Optional[int] = None, cache_seqlens: Optional[torch.Tenso
     positions 0 .. T - 1 (T: the whole cache by default). Returns (k, v)."""
     lib = load_library()
     ptrs, B, Hkv, Tk, bits, group, dev = _check_kvq(cache)
-    _require_cuda("k_codes", cache[0])
+    _require_cuda_cache(dev)
     T = Tk if T is None else int(T)
     if T < 1 or (cache_seqlens is None and T > Tk):
         raise ValueError(f"T must be >= 1, and at most the cache's {Tk} positions without cache_seqlens")
@@ -459,8 +464,11 @@ def kvq_read(cache, T: Optional[int] = None, cache_seqlens: Optional[torch.Tenso
 
     def call(handle):
         nonlocal out_k, out_v
-        out_k = cache[1].new_empty(shape) if out_k is None else out_k
-        out_v = cache[1].new_empty(shape) if out_v is None else out_v
+        strides = (T * Hkv * 128, Hkv * 128, 128, 1)
+        if out_k is None:
+            out_k = torch.empty_strided(shape, strides, dtype=torch.bfloat16, device=dev)
+        if out_v is None:
+            out_v = torch.empty_strided(shape, strides, dtype=torch.bfloat16, device=dev)
         return lib.attn_kvq_read(*ptrs, None if cache_seqlens is None else cache_seqlens.data_ptr(), out_k.data_ptr(),
                                  out_v.data_ptr(), B, T, Hkv, Tk, 128, bits, group, handle)
 
@@ -481,12 +489,10 @@ def attn_decode_kvq(q: torch.Tensor, cache, cache_seqlens: torch.Tensor, scale: 
     and values the codes stand for. cache_seqlens, grouped heads and window as for attn_decode. Returns
     (o [B, Tq, H, D], lse [B, H, Tq])."""
     lib = load_library()
-    _require_cuda("q", q)
-    _check_qkv("q", q)
     ptrs, B, Hkv, Tk, bits, group, dev = _check_kvq(cache)
+    _require_cuda_cache(dev)
+    _check_qkv("q", q, device=dev)
     Bq, Tq, H, D = q.shape
-    if q.device != dev:
-        raise ValueError(f"q is on {q.device}; every tensor of one call must be on {dev}")
     if Bq != B:
         raise ValueError(f"q has shape {tuple(q.shape)}; expected [{B}, Tq, H, {D}]")
     _check_seqlens(cache_seqlens, B, dev)
@@ -503,7 +509,8 @@ def attn_decode_kvq(q: torch.Tensor, cache, cache_seqlens: torch.Tensor, scale: 
     def call(handle):
         nonlocal out, out_lse
         out = torch.empty_like(q) if out is None else out
-        out_lse = q.new_empty((B, H, Tq), dtype=torch.float32) if out_lse is None else out_lse
+        if out_lse is None:
+            out_lse = torch.empty_strided((B, H, Tq), (H * Tq, Tq, 1), dtype=torch.float32, device=dev)
         ws = workspace
         if ws is None:
             need = _decode_kvq_workspace(B, H, Hkv, Tq, Tk, D)
