@@ -128,9 +128,9 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], uint32_t (&co
   const float span = __bfloat162float(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx))) - z;
   // Quotients by Markstein's method (IBM J. Res. Dev. 34, 1990): with y = 1 / b rounded to nearest and q = a y, the
   // sum q + (a - q b) y, the remainder exact, is a / b rounded to nearest. Nothing less will do: bf16 numbers over a
-  // bf16 scale lie on ties often (one in 50 at 4 bits). The compiler's divisions took 2.8 times as long (234 us against 83 for 32 x 2048
-  // tokens of 10 heads at 4 bits, groups of 32). Added to
-  // 1.5 * 2^23 a quotient is rounded to an integer in the sum's low bits.
+  // bf16 scale lie on ties often (one in 50 at 4 bits). The compiler's divisions took 2.8 times as long (234 us
+  // against 83 for 32 x 2048 tokens of 10 heads at 4 bits, groups of 32). Added to 1.5 * 2^23 a quotient is rounded
+  // to an integer in the sum's low bits.
   constexpr float kMagic = 12582912.f, kInverse = 1.f / kLevels;
   uint32_t t[16];
   if (span >= 0x1p-80f && span <= 0x1p100f) {
@@ -146,7 +146,7 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], uint32_t (&co
       t[2 * i] = static_cast<uint32_t>(n.v), t[2 * i + 1] = static_cast<uint32_t>(n.v >> 32);
     }
     *sz = (sbits >> 16) | (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
-  } else if (span < INFINITY) {  // an inverse or a remainder may not be a normal number; or a constant group: s and n are 0
+  } else if (span < INFINITY) {  // an inverse or a remainder may not be a normal number; constant group: s = n = 0
     const uint32_t sbits = (__float_as_uint(__fdiv_rn(span, kLevels)) + 0xffffu) & 0xffff0000u;
 #pragma unroll
     for (int i = 0; i < 16; ++i) t[i] = __float_as_uint(kMagic);
@@ -177,7 +177,8 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], uint32_t (&co
       for (int j = 6; j >= 0; --j) u = (u << 4) + t[8 * i + j];
       codes[i] = u - 0x4b400000u * 0x11111111u;
     } else {
-      codes[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040), __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040), 0x5410);
+      codes[i] = __byte_perm(__byte_perm(t[4 * i], t[4 * i + 1], 0x0040),
+                             __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040), 0x5410);
     }
   }
 }
@@ -186,7 +187,8 @@ template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kWriteThreads) kvq_write_kernel(const CopyParams p) {
   begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
-  const uint32_t c = threadIdx.x % kWriteLanes, r = blockIdx.x * (kWriteThreads / kWriteLanes) + threadIdx.x / kWriteLanes;
+  const uint32_t c = threadIdx.x % kWriteLanes;
+  const uint32_t r = blockIdx.x * (kWriteThreads / kWriteLanes) + threadIdx.x / kWriteLanes;
   const uint32_t rows = static_cast<uint32_t>(p.B) * p.T * p.Hkv;
   const size_t n_new = static_cast<size_t>(rows) * 128, n_cache = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_new, (void)n_cache;
@@ -206,7 +208,8 @@ __global__ void __launch_bounds__(kWriteThreads) kvq_write_kernel(const CopyPara
   }
   const size_t to = at.cache * static_cast<size_t>(kRowBytes) + c * (2 * kBits);
   const size_t sz_to = at.cache * static_cast<size_t>(kGroups) + 16 * c / kGroup;
-  const bool write = live && at.there && ATTN_IN_RANGE(to, 2 * kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error) &&
+  const bool write = live && at.there &&
+                     ATTN_IN_RANGE(to, 2 * kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error) &&
                      ATTN_IN_RANGE(sz_to, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -258,8 +261,12 @@ __global__ void __launch_bounds__(kReadThreads) kvq_read_kernel(const CopyParams
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // dims 2 i and 2 i + 1
       float n0, n1;
-      if constexpr (kBits == 4) n0 = number(even, i), n1 = number(odd, i);
-      else n0 = number(i < 2 ? codes[t].x : codes[t].y, 2 * (i % 2)), n1 = number(i < 2 ? codes[t].x : codes[t].y, 2 * (i % 2) + 1);
+      if constexpr (kBits == 4) {
+        n0 = number(even, i), n1 = number(odd, i);
+      } else {
+        const uint32_t w = i < 2 ? codes[t].x : codes[t].y;
+        n0 = number(w, 2 * (i % 2)), n1 = number(w, 2 * (i % 2) + 1);
+      }
       out[i] = as_u32(__floats2bfloat162_rn(fmaf(n0, s, z), fmaf(n1, s, z)));
     }
     *reinterpret_cast<uint4*>(p.y[t] + to) = make_uint4(out[0], out[1], out[2], out[3]);
@@ -367,8 +374,8 @@ attn_status check_decode(int B, int H, int Hkv, int Tq, int Tk, int D, int bits,
   if (st != ATTN_OK) return st;
   if ((H / Hkv) * static_cast<long long>(Tq) > attn::kKvqMaxRows) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H * Tq > 0x7fffffffLL / 8) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL / Tk) return ATTN_ERR_UNSUPPORTED;  // cache rows, as for write and read
-  // the row of all places (a unit's tiles, 16 keys or more each, and a few) is counted in 30 bits
+  // cache rows are counted in 31 bits, the row of all places (a unit's tiles, 16 keys or more each, and a few) in 30
+  if (static_cast<long long>(B) * Hkv > 0x7fffffffLL / Tk) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Hkv > (1LL << 30) / (Tk / 16 + 1 + attn::kKvqUnitCost)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
@@ -378,12 +385,12 @@ int decode_span(int Tq, int Tk, int window) {
   return window < 0 ? Tk : static_cast<int>(std::min<long long>(Tk, static_cast<long long>(Tq) + window));
 }
 
-// How a decode call is split: the split kernel's CTAs, one per SM or fewer where there is not a 16-key tile for every warp,
-// and whether each of them has whole units. That spares the merge kernel but leaves CTAs uneven, or idle where there are
-// fewer units, so it is for small calls: up to 8 tiles of 16 keys a warp where there are units for (nearly) all CTAs, else
-// up to 4. Measured, whole / split: 640 units of 200 keys 11.4 / 13.8 us, of 1 to 200 keys 11.8 / 12.6; 140 units of 192
-// keys 6.9 / 9.2, of 1,500 keys 12.6 / 13.8, of 1 to 2,000 keys (over the limit) 14.2 / 12.4; 10 units of 384 keys
-// 7.3 / 8.8, of 1,500 keys (over it) 12.0 / 9.1.
+// How a decode call is split: the split kernel's CTAs, one per SM or fewer where there is not a 16-key tile for every
+// warp, and whether each of them has whole units. That spares the merge kernel but leaves CTAs uneven, or idle where
+// there are fewer units, so it is for small calls: up to 8 tiles of 16 keys a warp where there are units for (nearly)
+// all CTAs, else up to 4. Measured, whole / split: 640 units of 200 keys 11.4 / 13.8 us, of 1 to 200 keys 11.8 /
+// 12.6; 140 units of 192 keys 6.9 / 9.2, of 1,500 keys 12.6 / 13.8, of 1 to 2,000 keys (over the limit) 14.2 / 12.4;
+// 10 units of 384 keys 7.3 / 8.8, of 1,500 keys (over it) 12.0 / 9.1.
 struct DecodeSplit {
   unsigned ctas;
   bool whole;

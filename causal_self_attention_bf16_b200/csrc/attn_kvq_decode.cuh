@@ -1,13 +1,14 @@
 // Attention of a few new queries over the quantised key/value cache (include/attn.h, attn_decode_kvq): the cached
 // decode of attn_decode with keys and values held as 4- or 8-bit codes n that stand for n * s + z per group of dims.
 //
-// The cache is read once and bounds the call: a key and its value are 2 * (16 * bits + 512 / group) bytes, 136 to
-// 160 at 4 bits, and at the 6.56 TB/s of an HBM copy an SM gets about 23 bytes per clock, a 16-key tile every 105
-// clocks. CUDA cores alone cannot turn 4,096 codes into products in that time (two operations a code are 64 clocks
-// of every lane), so the codes go to the matrix unit, as A fragments of mma.m16n8k16 (fp16 in, fp32 sums) made in
-// registers. tcgen05 would need them widened in shared or tensor memory first, four bytes written for every byte
-// read, to fill 128-row tiles with 1 to 32 queries. What bounds the loop is the widening itself, so it is kept to
-// few operations, spread over the integer and the floating-point pipe:
+// The cache is read once and bounds the call: a key and its value are 2 * (16 * bits + 512 / group) bytes, 136 to 160
+// at 4 bits, and at the 6.56 TB/s of an HBM copy an SM gets about 23 bytes per clock, a 16-key tile every 105 clocks.
+// CUDA cores alone cannot turn 4,096 codes into products in that time (two operations a code are 64 clocks of every
+// lane), so the codes go to the matrix unit, as A fragments of mma.m16n8k16 (fp16 in, fp32 sums) made in registers.
+// tcgen05 would need them widened in shared or tensor memory first, four bytes written for every byte read, to fill
+// 128-row tiles with 1 to 32 queries. What bounds the loop at 4 bits is the memory and the widening together, so that
+// is kept to few operations. 256 sequences of 1,024 to 2,048 keys with 10 heads, groups of 64: 107 us, 5.3 TB/s (81 %
+// of the copy); 95 us with the arithmetic taken out. Long runs meet the power cap, 122 us at 1.73 GHz.
 //
 //   Codes. A small integer in the low bits of an fp16 number is that number: n * 2^-24, a subnormal, which the matrix
 //   unit multiplies exactly. So one logical operation makes two numbers of a 32-bit word's low nibbles (n * 2^-24), of
@@ -16,21 +17,25 @@
 //   Scores. For key j and query row r, with the sums taken group by group of dims:
 //     q . k = sum_g s_g (sum_d q_d n_d) + z_g (sum_d q_d).     The first sum is the matrix product, the last is made
 //   once per query row. A query row is scaled by a power of two that puts its largest dim into [2^14, 2^15), so that
-//   its bf16 numbers are fp16 numbers (exactly down to 2^-34 of the largest); the power goes off with the softmax scale.
-//   Values. o = sum_j p_j s_g (n - c) + sum_j p_j (z_g + c s_g), c = 8 or 128: one packed addition centres the codes, so
-//   that the fp32 accumulators hold sums of both signs, whose roundings stay small however long the cache. p_j s_g is
-//   the B fragment, rounded to fp16: 2^-11 of itself at most against the output's own 2^-8. So that it is in fp16's
-//   range whatever the scales, it is carried in units of a power of two per group of dims, raised when a key's scale
-//   passes it by 2^5 (and the sums rescaled). The second sum is fp32 throughout.
+//   its bf16 numbers are fp16 numbers (exactly down to 2^-34 of the largest); the power goes off with the softmax
+//   scale. The unit aligns products by their factors' exponent fields, so a subnormal factor's leading zeros are bits
+//   that small products of a sum lose: with the codes lse stays within 5e-7 of itself, but the queries' sums, whose
+//   other factor could be as small as 2^-24, are made with 1 (lse was off by 2e-6 otherwise).
+//   Values. o = sum_j p_j s_g (n - c) + sum_j p_j (z_g + c s_g), c = 8 or 128: one packed addition centres the codes,
+//   so that the fp32 accumulators hold sums of both signs: they are cut off, not rounded (1 + 1.5 * 2^-24 stays 1),
+//   which sums of one sign over a whole cache would show. p_j s_g is the B fragment, rounded to fp16: 2^-11 of itself
+//   at most against the output's own 2^-8. So that it is in fp16's range whatever the scales, it is carried in units
+//   of a power of two per group of dims, raised when a key's scale passes it by 2^6 (and the sums rescaled). The
+//   second sum is fp32 throughout.
 //   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 8 (then p <= 2^8
 //   and the sums stay far from overflow): one vote a tile in place of the reduction and the rescaling.
 //
-// Work split. A unit is one (sequence, key/value head); its visible keys, tiles of 32 (8 bits: 16). All units' tiles in a
-// row, with a place more for each unit's own cost, are dealt to the warps in equal stretches, found on the device from
-// the lengths, so that every warp has the same work however ragged the batch, through a ring of tiles in shared memory
-// that it fills for itself (cp.async; no barrier in the loop). A unit that begins and ends in one warp's stretch is
-// finished there; the pieces of one that spans warps are joined by the CTA at its end, and the CTAs' pieces by
-// kvq_decode_merge_kernel.
+// Work split. A unit is one (sequence, key/value head); its visible keys, tiles of 32 (8 bits: 16). All units' tiles
+// in a row, with two places more for each unit's own cost, are dealt to the warps in equal stretches, found on the
+// device from the lengths, so that every warp has the same work however ragged the batch, through a ring of tiles in
+// shared memory that it fills for itself (cp.async; no barrier in the loop). A unit that begins and ends in one
+// warp's stretch is finished there; the pieces of one that spans warps are joined by the CTA at its end, and the
+// CTAs' pieces by kvq_decode_merge_kernel.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -108,7 +113,8 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
 // The same with c = 0 before.
 __device__ __forceinline__ void mma_16x8x16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                   uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+               "{%10,%10,%10,%10};"
                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
@@ -207,8 +213,8 @@ __device__ __forceinline__ float kvq_inverse(float x) { return __uint_as_float((
 
 // ------------------------------------------------------------------------------------------------ layout
 
-// A tile in shared memory: 16 key rows of codes, 16 value rows, then 16 rows of key and of value params. Chunk c (16
-// bytes) of row r sits at chunk c ^ kvq_swizzle(r). A score tile's row g is key kvq_key(g) (rows 8-15: + 8). With
+// A tile in shared memory: its key rows of codes, its value rows, then a row of key and of value params each. Chunk c
+// (16 bytes) of row r sits at chunk c ^ kvq_swizzle(r). A score tile's row g is key kvq_key(g) (rows 8-15: + 8). With
 // these two every read below, 4 to 16 bytes a lane, meets each bank once: the eight keys of a row set, and the four
 // that a half (or quarter) warp reads together, fall into different banks.
 template <int kBits>
@@ -272,22 +278,25 @@ __device__ __forceinline__ void kvq_next_unit(const KvqDecodeParams& p, KvqCurso
 
 // ------------------------------------------------------------------------------------------------ split kernel
 
-// A warp takes up to 8 query rows; with more, n_rt = ceil(R / 8) warps take a stretch's tiles together.
+// A warp takes up to 8 query rows; with more, n_rt = ceil(R / 8) warps take a stretch's tiles together, each for itself
+// (32 rows: 24 us where the bytes would take 2.3). 12 warps of 168 registers an SM: 16 of 128 took half as many
+// instructions again.
 template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const KvqDecodeParams p) {
   using Shape = KvqShape<kBits, kGroup>;
   constexpr int kGroups = Shape::kGroups, kRowBytes = Shape::kRowBytes, kStages = Shape::kStages;
   constexpr int kHalves = Shape::kHalves, kTile = Shape::kTile;
   constexpr int kWords = kGroup * kBits / 128;   // 32-bit words of a key row and group that a lane scores
-  constexpr int kVWords = kGroup * kBits / 256;  // words of a value row and group that a lane multiplies (0: half a word)
+  constexpr int kVWords = kGroup * kBits / 256;  // of a value row and group that a lane multiplies (0: half a word)
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
   constexpr float kNone = -3e38f;                // running max before the first key
   extern __shared__ __align__(128) uint8_t kvq_smem[];
   __shared__ KvqPiece sh_piece[2 * kKvqWarps];  // stretch i's slots at 2 i, 2 i + 1
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int R = p.R, G = p.H / p.Hkv;
-  asm volatile("griddepcontrol.wait;" ::: "memory");               // (this grid may be launched before the one it follows ends)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge kernel waits for this grid's end)
+  // This grid may be launched before the one it follows ends; the merge kernel in turn waits for this grid's end.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n_rt = (R + 7) / 8;
   const int slices = kKvqWarps / n_rt;  // stretches per CTA, each for the n_rt warps of its row tiles
   const int rt = warp % n_rt, slice = warp / n_rt;
@@ -314,10 +323,12 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  const int stretches = (p.whole ? 1 : static_cast<int>(gridDim.x)) * slices, stretch0 = p.whole ? 0 : blockIdx.x * slices;
-  // Stretch i of all begins at place i * total / stretches, rounded down (the half place keeps the product's rounding away
-  // from whole numbers), so that every CTA has the same number of places, to one; with fewer places than stretches the
-  // first ones have one each. No stretch before another's end is empty. A stretch's tiles are those whose places it has.
+  const int stretches = (p.whole ? 1 : static_cast<int>(gridDim.x)) * slices;
+  const int stretch0 = p.whole ? 0 : blockIdx.x * slices;
+  // Stretch i of all begins at place i * total / stretches, rounded down (the half place keeps the product's rounding
+  // away from whole numbers), so that every CTA has the same number of places, to one; with fewer places than
+  // stretches the first ones have one each. No stretch before another's end is empty. A stretch's tiles are those
+  // whose places it has.
   auto begin_of = [&](int i) {
     if (total <= stretches || i >= stretches) return min(i < stretches ? i : total, total);
     return static_cast<int>((static_cast<double>(static_cast<long long>(i) * total) + 0.5) * p.per_stretch);
@@ -353,7 +364,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   // --- the ring
   const uint32_t ring = sm100::smem_u32(kvq_smem) + warp * kStages * Shape::kStageBytes;
   constexpr int kChunks = kRowBytes / 16, kRowsAtOnce = 32 / kChunks;  // 16-byte chunks of a row; rows a copy covers
-  const int c_row = lane / kChunks, p_row = lane % 16;  // (params: 16 rows of keys by the lower lanes, of values by the upper)
+  const int c_row = lane / kChunks, p_row = lane % 16;  // (params: key rows by the lower lanes, value rows by the upper)
   // (a copy's rows are a multiple of 4 apart, and of 8 where the swizzle looks at bit 2)
   uint32_t code_at[kTile / kRowsAtOnce];
 #pragma unroll
@@ -434,7 +445,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   const uint32_t v0_lds = Shape::kCodeBytes + at_byte(vk0, v_byte), v1_lds = Shape::kCodeBytes + at_byte(vk1, v_byte);
 
   auto piece_o = [&](int slot, int w) {  // [8][128]
-    return reinterpret_cast<float*>(kvq_smem + (slot ? w * kStages * Shape::kStageBytes : Shape::kRing + w * Shape::kPiece));
+    return reinterpret_cast<float*>(
+        kvq_smem + (slot ? w * kStages * Shape::kStageBytes : Shape::kRing + w * Shape::kPiece));
   };
   auto piece_ml = [&](int slot, int w) {  // [8][2]
     return reinterpret_cast<float*>(kvq_smem + Shape::kRing + kKvqWarps * Shape::kPiece) + (slot * kKvqWarps + w) * 16;
@@ -452,7 +464,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
     // key row that it reads, paired as the codes are, in units of 2^-up (4 bits: second and fourth nibbles 2^(4 - up),
     // as their codes are 2^4 larger).
     uint32_t qb[16];
-    float qsum[kGroups][2];  // per group, the sum of q over its dims in units of 2^(24 - up), of columns 2 t and 2 t + 1
+    float qsum[kGroups][2];  // a group's sum of q over its dims, units of 2^(24 - up), of columns 2 t and 2 t + 1
     float down[2];           // softmax scale (log2 units) times 2^(24 - up) of columns 2 t and 2 t + 1
     {
       const int row = rt * 8 + g, i = p.row_i[row], h = cur.hk * G + p.row_g[row];
@@ -811,10 +823,10 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         }
         if (r == 0 && lane == 0 && begins)  // it begins here and goes on past this CTA
         {
-          int c = min(static_cast<int>(static_cast<double>(end - 1) / (static_cast<double>(total) * p.per_stretch)) / slices,
-                      static_cast<int>(gridDim.x) - 1);  // the CTA of its last place
+          // the CTA of its last place, to one
+          int c = static_cast<int>(static_cast<long long>(end - 1) * gridDim.x / total);
           while (c > 0 && begin_of(c * slices) >= end) --c;
-          while (begin_of((c + 1) * slices) < end) ++c;
+          while (begin_of((c + 1) * slices) < end) ++c;  // (ends: begin_of(gridDim.x * slices) is the row's end)
           p.spans[blockIdx.x] = KvqSpan{unit, c, slot, 0};
         }
       }
@@ -824,10 +836,10 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 
 // ------------------------------------------------------------------------------------------------ merge kernel
 
-// Block (x, y): rows kRows y .. kRows (y + 1) - 1 of the unit that begins in the split kernel's CTA x and goes on past it,
-// if there is one: O = sum_s O_s 2^(m_s - M) / sum_s l_s 2^(m_s - M) over its pieces, M = max_s m_s. The block's 8 warps
-// share the rows and, where there are fewer rows, each row's pieces; a lane takes four dims. A running maximum as in the
-// split kernel, so that a piece is read once, with its maximum and sum.
+// Block (x, y): rows kRows y .. kRows (y + 1) - 1 of the unit that begins in the split kernel's CTA x and goes on
+// past it, if there is one: O = sum_s O_s 2^(m_s - M) / sum_s l_s 2^(m_s - M) over its pieces, M = max_s m_s. The
+// block's 8 warps share the rows and, where there are fewer rows, each row's pieces; a lane takes four dims. A
+// running maximum as in the split kernel, so that a piece is read once, with its maximum and sum.
 template <int kRows>
 __global__ void __launch_bounds__(256) kvq_decode_merge_kernel(const KvqDecodeParams p) {
   constexpr int kSlices = 8 / kRows;  // warps that share a row's pieces

@@ -90,14 +90,14 @@ def write_call(lib, ptrs, **kw):
     names = ["k", "v", "kc", "kp", "vc", "vp", "lens"]
     a = dict(zip(names, ptrs), B=B, T=T, hkv=HKV, Tk=TK, D=128, bits=4, group=32)
     a.update(kw)
-    return lib.attn_kvq_write(*[a[n] for n in names], *[a[n] for n in ("B", "T", "hkv", "Tk", "D", "bits", "group")], None)
+    return lib.attn_kvq_write(*[a[n] for n in (*names, "B", "T", "hkv", "Tk", "D", "bits", "group")], None)
 
 
 def read_call(lib, ptrs, **kw):
     names = ["kc", "kp", "vc", "vp", "lens", "k", "v"]
     a = dict(zip(names, ptrs), B=B, T=T, hkv=HKV, Tk=TK, D=128, bits=4, group=32)
     a.update(kw)
-    return lib.attn_kvq_read(*[a[n] for n in names], *[a[n] for n in ("B", "T", "hkv", "Tk", "D", "bits", "group")], None)
+    return lib.attn_kvq_read(*[a[n] for n in (*names, "B", "T", "hkv", "Tk", "D", "bits", "group")], None)
 
 
 def test_write_and_read_argument_errors(lib):
@@ -135,8 +135,8 @@ def decode_call(lib, ptrs, wb, **kw):
     names = ["q", "kc", "kp", "vc", "vp", "lens", "o", "lse", "w"]
     a = dict(zip(names, ptrs), wb=wb, B=2, H=8, hkv=2, Tq=2, Tk=1000, D=128, bits=4, group=64, scale=0.088, window=-1)
     a.update(kw)
-    return lib.attn_decode_kvq(*[a[n] for n in names], a["wb"],
-                               *[a[n] for n in ("B", "H", "hkv", "Tq", "Tk", "D", "bits", "group", "scale", "window")], None)
+    return lib.attn_decode_kvq(*[a[n] for n in (*names, "wb", "B", "H", "hkv", "Tq", "Tk", "D", "bits", "group",
+                                                "scale", "window")], None)
 
 
 def test_decode_argument_errors(lib):
@@ -172,9 +172,9 @@ def test_decode_sizes_refused_by_the_host_queries(lib):
 
 
 def test_decode_split_rule(lib):
-    """Small calls are whole units, one kernel without a workspace: up to 8 tiles of 16 keys for each of a CTA's 12 warps
-    where the units fill three quarters of 148 CTAs, else 4 (the warps shared by the row tiles of 8 query rows). Others
-    are split over up to 148 CTAs: a span (16 bytes) per CTA, and two pieces of 130 floats per CTA and row."""
+    """Small calls are whole units, one kernel without a workspace: up to 8 tiles of 16 keys for each of a CTA's 12
+    warps where the units fill three quarters of 148 CTAs, else 4 (the warps shared by the row tiles of 8 query rows).
+    Others are split over up to 148 CTAs: a span (16 bytes) per CTA, and two pieces of 130 floats per CTA and row."""
     ws, kern = lib.attn_decode_kvq_workspace_bytes, lib.attn_decode_kvq_kernels
     for B, H, hkv, Tq, Tk, whole in ((3, 4, 2, 2, 300, True),      # 6 units of 19 tiles
                                      (1, 10, 10, 1, 768, True),    # 10 units of 48 tiles: 4 a warp

@@ -122,7 +122,8 @@ def test_write_codes_are_the_formula_bit_for_bit(bits, group):
     rows of every size (2^-90 to 2^90), on coarse grids where ties are common, and each of the 128 scale mantissas."""
     g = torch.Generator().manual_seed(100 * bits + group)
     x = torch.randn(4000, 128, generator=g) * torch.exp2(torch.randint(-90, 91, (4000, 1), generator=g).float())
-    grid = torch.randint(-300, 300, (3000, 128), generator=g).float() * torch.exp2(torch.randint(-20, 20, (3000, 1), generator=g).float())
+    grid = torch.randint(-300, 300, (3000, 128), generator=g).float()
+    grid *= torch.exp2(torch.randint(-20, 20, (3000, 1), generator=g).float())
     # a span of m * 2^k * levels has the scale m * 2^k: m in [1, 2) in steps of 2^-7, the rest of the group on halves
     m = 1 + torch.arange(128).float() / 128
     lanes = torch.arange(128) % group
@@ -224,8 +225,8 @@ def check_decode(q, cache, lens, scale, window, o, lse, what):
     for b, L in enumerate(min(max(L, 0), Tk) for L in lens):
         for h in range(H):
             k, v = (dequantize(t[b, h // G, :L].numpy(), p[b, h // G, :L], bits) for t, p in ((kc, kp), (vc, vp)))
-            ks, vs = (np.repeat(np.abs(cpu(p[b, h // G, :L, :, 1])) + c * cpu(p[b, h // G, :L, :, 0]), D // p.shape[3], -1)
-                      for p in (kp, vp))
+            ks, vs = (np.repeat(np.abs(cpu(p[b, h // G, :L, :, 1])) + c * cpu(p[b, h // G, :L, :, 0]),
+                                D // p.shape[3], -1) for p in (kp, vp))
             vstep = np.repeat(cpu(vp[b, h // G, :L, :, 0]), D // vp.shape[3], -1)
             for i in range(Tq):
                 last = L - Tq + i
@@ -307,8 +308,8 @@ def test_decode_many_short_sequences(bits, group, Tk):
 @pytest.mark.parametrize("Tk", [768, 769])
 @pytest.mark.parametrize("H,Tq", [(1, 1), (3, 4), (8, 4)])
 def test_decode_on_both_sides_of_the_split_rule(Tk, H, Tq):
-    """The same keys in whole units and split over CTAs (a capacity past the rule's limit): the oracle's result, and each
-    other's up to the rounding of the joined sums."""
+    """The same keys in whole units and split over CTAs (a capacity past the rule's limit): the oracle's result, and
+    each other's up to the rounding of the joined sums."""
     lens = [700, 31]
     q, cache, o, lse = run_decode(2, H, 1, Tq, Tk, 4, 64, lens)
     wide = attn.kvq_cache(2, 1, 4000, 4, 64)
@@ -352,9 +353,11 @@ def test_refusals_on_the_device():
     for call in (lambda: attn.kvq_write(cache, k.half(), k, lens), lambda: attn.kvq_write(cache, k, k[:, :3], lens),
                  lambda: attn.kvq_write(cache, k[:, :, :2].contiguous(), k[:, :, :2].contiguous(), lens),
                  lambda: attn.kvq_write(cache, k[:1], k[:1], lens), lambda: attn.kvq_write(cache, k, k, lens.long()),
-                 lambda: attn.kvq_write(cache, k, k, lens.cpu()), lambda: attn.kvq_write(cache, k.transpose(1, 2), k, lens),
-                 lambda: attn.kvq_read(cache, 0), lambda: attn.kvq_read(cache, 9), lambda: attn.kvq_read(cache, 4, lens[:1]),
-                 lambda: attn.kvq_read(cache, 4, lens, k.float(), k), lambda: attn.kvq_read(cache, 4, lens, k[:, :3], k),
+                 lambda: attn.kvq_write(cache, k, k, lens.cpu()),
+                 lambda: attn.kvq_write(cache, k.transpose(1, 2), k, lens),
+                 lambda: attn.kvq_read(cache, 0), lambda: attn.kvq_read(cache, 9),
+                 lambda: attn.kvq_read(cache, 4, lens[:1]), lambda: attn.kvq_read(cache, 4, lens, k.float(), k),
+                 lambda: attn.kvq_read(cache, 4, lens, k[:, :3], k),
                  lambda: attn.attn_decode_kvq(q.float(), cache, lens), lambda: attn.attn_decode_kvq(q[:1], cache, lens),
                  lambda: attn.attn_decode_kvq(q, cache, lens, window=-1),
                  lambda: attn.attn_decode_kvq(q, cache, lens, o=q[:, :, :3]),
@@ -556,5 +559,19 @@ def test_offsets_past_32_bits():
     clean()
     tail = tuple(torch.stack([t[0, :, :40], t[1, :, Tk - 40:]]) for t in cache)
     check_decode(q, tail, [5, 40], 128 ** -0.5, 39, o, lse, "past 32 bits")
-    del cache
+    # every key 0 and every value 1.5: lse is the logarithm of the length, o is 1.5
+    cache.k_params.zero_()
+    cache.v_params[..., 0] = 0
+    cache.v_params[..., 1] = 1.5
+    o, lse = attn.attn_decode_kvq(q, cache, lens)
+    clean()
+    assert (o == 1.5).all()
+    assert np.abs(cpu(lse) - np.log([[[5], [5]], [[Tk], [Tk]]])).max() <= 2.0 ** -18
+    # the whole cache read back, 8.6 GB a tensor: first, middle and last rows of each sequence
+    cache.v_params[1, 1, Tk - 1] = 7
+    rk, rv = attn.kvq_read(cache)
+    clean()
+    assert (rk[:, ::100001] == 0).all() and (rv[:, :-1:100001] == 1.5).all()
+    assert (rv[0, -1] == 1.5).all() and (rv[1, -1, 0] == 1.5).all() and (rv[1, -1, 1] >= 7).all()
+    del cache, rk, rv
     torch.cuda.empty_cache()
