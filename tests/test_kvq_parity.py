@@ -505,6 +505,41 @@ def test_steps_captured_in_a_graph():
         assert torch.equal(o, ref[i][0]) and torch.equal(lse, ref[i][1]), f"step {i}"
 
 
+def test_capture_of_a_forked_step_and_of_two_graphs():
+    """A captured step whose calls follow copies, a memset and another stream's kernels: the write on a side stream that
+    joins before the decode, default workspace and outputs. Two such graphs replayed in turn keep their results apart."""
+    B, H, Hkv, Tk, lens0 = 3, 4, 2, 3000, [2000, 5, 2999]
+    k, v, q = (randn((2, B, 1, h, 128), 100 + j).cuda() for j, h in enumerate((Hkv, Hkv, H)))
+    caches = [filled(B, Hkv, Tk, bits, 64, lens0, 110 + bits) for bits in (4, 8)]
+    ref = []
+    for i, cache in enumerate(caches):
+        copy = tuple(t.clone() for t in cache)
+        attn.kvq_write(copy, k[i], v[i], ints(lens0) + 1)
+        ref.append((*attn.attn_decode_kvq(q[i], copy, ints(lens0) + 1), *attn.kvq_read(copy, 3, ints(lens0))))
+    lens_in, lens, qs, side = ints(lens0), ints([0] * B), torch.empty_like(q[0]), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for i, cache in enumerate(caches):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lens.copy_(lens_in)
+            lens += 1
+            side.wait_stream(torch.cuda.current_stream())
+            attn.kvq_write(cache, k[i], v[i], lens, stream=side)
+            qs.zero_()
+            qs.copy_(q[i])
+            torch.cuda.current_stream().wait_stream(side)
+            o, lse = attn.attn_decode_kvq(qs, cache, lens)
+            lens -= 1
+            outs.append((o, lse, *attn.kvq_read(cache, 3, lens)))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph, out, want in zip(graphs, outs, ref):
+            graph.replay()
+            clean()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 def test_calls_on_another_stream():
     """Every call with stream=: ordered on that stream, outputs made there belong to it."""
     B, H, Hkv, Tk = 2, 4, 2, 4000
