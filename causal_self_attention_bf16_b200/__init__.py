@@ -11,6 +11,7 @@ include/attn.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -372,30 +373,45 @@ def kvq_cache(B: int, H_kv: int, Tk: int, bits: int = 4, group: int = 64, device
 
 def _check_kvq(cache):
     """Check the cache's four tensors (all on one device). Returns (their pointers, B, H_kv, Tk, bits, group,
-    device)."""
+    device). What a decode loop passes every time is looked over once; _explain_kvq says what is wrong otherwise."""
+    try:
+        kc, kp, vc, vp = cache
+        dev, cs, ps = kc.device, kc.shape, kp.shape
+        B, Hkv, Tk, row = cs
+        groups = ps[3]
+        good = (isinstance(cache, (tuple, list)) and kc.dtype is vc.dtype is torch.uint8
+                and kp.dtype is vp.dtype is torch.bfloat16 and row in (64, 128) and groups in (1, 2, 4)
+                and ps == (B, Hkv, Tk, groups, 2) and vc.shape == cs and vp.shape == ps and B and Hkv and Tk
+                and kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous() and vp.is_contiguous()
+                and kp.device == dev and vc.device == dev and vp.device == dev)
+    except (AttributeError, IndexError, TypeError, ValueError):
+        good = False
+    if not good:
+        raise ValueError(_explain_kvq(cache))
+    return (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), B, Hkv, Tk, row // 16, 128 // groups, dev
+
+
+def _explain_kvq(cache) -> str:
+    """What is wrong with a cache that _check_kvq does not take."""
     if not isinstance(cache, (tuple, list)) or len(cache) != 4:
-        raise ValueError("cache must be a KVQCache or a tuple (k_codes, k_params, v_codes, v_params)")
-    for t in cache:
-        if not isinstance(t, torch.Tensor):
-            raise ValueError("cache must hold four tensors (k_codes, k_params, v_codes, v_params)")
+        return "cache must be a KVQCache or a tuple (k_codes, k_params, v_codes, v_params)"
+    if not all(isinstance(t, torch.Tensor) for t in cache):
+        return "cache must hold four tensors (k_codes, k_params, v_codes, v_params)"
     kc, kp, vc, vp = cache
     dev, cs, ps = kc.device, kc.shape, kp.shape
     if len(cs) != 4 or cs[3] not in (64, 128) or 0 in cs:
-        raise ValueError(f"k_codes has shape {tuple(cs)}; expected [B, H_kv, Tk, 64] (4 bits) or [.., 128] (8 bits)")
-    B, Hkv, Tk, row = cs
+        return f"k_codes has shape {tuple(cs)}; expected [B, H_kv, Tk, 64] (4 bits) or [.., 128] (8 bits)"
+    B, Hkv, Tk, _ = cs
     groups = ps[3] if len(ps) == 5 else 0
     if groups not in (1, 2, 4) or ps != (B, Hkv, Tk, groups, 2):
-        raise ValueError(f"k_params has shape {tuple(ps)}; expected [{B}, {Hkv}, {Tk}, 128 // group, 2]")
-    if not (kc.dtype == vc.dtype == torch.uint8 and kp.dtype == vp.dtype == torch.bfloat16 and vc.shape == cs
-            and vp.shape == ps and kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous()
-            and vp.is_contiguous() and kp.device == dev and vc.device == dev and vp.device == dev):
-        for name, t, shape, dtype in (("k_codes", kc, cs, torch.uint8), ("k_params", kp, ps, torch.bfloat16),
-                                      ("v_codes", vc, cs, torch.uint8), ("v_params", vp, ps, torch.bfloat16)):
-            if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor")
-            if t.device != dev:
-                raise ValueError(f"{name} is on {t.device}; every tensor of one call must be on {dev}")
-    return (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()), B, Hkv, Tk, row // 16, 128 // groups, dev
+        return f"k_params has shape {tuple(ps)}; expected [{B}, {Hkv}, {Tk}, 128 // group, 2]"
+    for name, t, shape, dtype in (("k_codes", kc, cs, torch.uint8), ("k_params", kp, ps, torch.bfloat16),
+                                  ("v_codes", vc, cs, torch.uint8), ("v_params", vp, ps, torch.bfloat16)):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            return f"{name} must be a contiguous {dtype} {list(shape)} tensor"
+        if t.device != dev:
+            return f"{name} is on {t.device}; every tensor of one call must be on {dev}"
+    return "cache must hold plain tensors"
 
 
 def _require_cuda_cache(dev: torch.device) -> None:
@@ -409,19 +425,25 @@ def _check_seqlens(cache_seqlens, B: int, dev: torch.device):
         raise ValueError("cache_seqlens must be a contiguous int32 [B] tensor on the cache's device")
 
 
-def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], call):
-    """call(stream handle) with `dev` current, and `stream`, where given, the current stream too, so that what the call
-    allocates belongs to the stream that uses it."""
-    if stream is None and torch.cuda.current_device() == dev.index:  # nothing to change, as in a decode loop
-        return call(_raw_stream(dev.index))
+# The current device, and the handle of a device's current stream without making a Stream object of it.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _elsewhere(dev: torch.device, stream: Optional[torch.cuda.Stream]) -> bool:
+    """Whether a call is to be made again inside _on: `dev` is not the current device, or a stream is named. (In a
+    decode loop it is not, and nothing has to be changed and put back.)"""
+    return stream is not None or _current_device() != dev.index
+
+
+@contextlib.contextmanager
+def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
+    """`dev` is current, and `stream`, where given, the current stream too, so that what the call allocates belongs to
+    the stream that uses it."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}; the call's tensors are on {dev}")
     with torch.cuda.device(dev), torch.cuda.stream(stream):
-        return call(_raw_stream(dev.index) if stream is None else stream.cuda_stream)
-
-
-def _raw_stream(index: int) -> int:
-    """The handle of the device's current stream."""
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (without making a Stream object)
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+        yield
 
 
 def kvq_write(cache, k: torch.Tensor, v: torch.Tensor, cache_seqlens: torch.Tensor,
@@ -438,8 +460,11 @@ def kvq_write(cache, k: torch.Tensor, v: torch.Tensor, cache_seqlens: torch.Tens
         raise ValueError(f"k has shape {tuple(k.shape)}; expected [{B}, T, {Hkv}, {D}]")
     _check_qkv("v", v, k.shape, dev)
     _check_seqlens(cache_seqlens, B, dev)
-    _check("attn_kvq_write", _launch(dev, stream, lambda handle: lib.attn_kvq_write(
-        k.data_ptr(), v.data_ptr(), *ptrs, cache_seqlens.data_ptr(), B, T, Hkv, Tk, D, bits, group, handle)))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kvq_write(cache, k, v, cache_seqlens)
+    _check("attn_kvq_write", lib.attn_kvq_write(k.data_ptr(), v.data_ptr(), *ptrs, cache_seqlens.data_ptr(), B, T, Hkv,
+                                                Tk, D, bits, group, _raw_stream(dev.index)))
 
 
 def kvq_read(cache, T: Optional[int] = None, cache_seqlens: Optional[torch.Tensor] = None,
@@ -460,20 +485,18 @@ def kvq_read(cache, T: Optional[int] = None, cache_seqlens: Optional[torch.Tenso
     for name, t in (("k", k), ("v", v)):
         if t is not None:
             _check_qkv(name, t, shape, dev)
-    out_k, out_v = k, v
-
-    def call(handle):
-        nonlocal out_k, out_v
-        strides = (T * Hkv * 128, Hkv * 128, 128, 1)
-        if out_k is None:
-            out_k = torch.empty_strided(shape, strides, dtype=torch.bfloat16, device=dev)
-        if out_v is None:
-            out_v = torch.empty_strided(shape, strides, dtype=torch.bfloat16, device=dev)
-        return lib.attn_kvq_read(*ptrs, None if cache_seqlens is None else cache_seqlens.data_ptr(), out_k.data_ptr(),
-                                 out_v.data_ptr(), B, T, Hkv, Tk, 128, bits, group, handle)
-
-    _check("attn_kvq_read", _launch(dev, stream, call))
-    return out_k, out_v
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kvq_read(cache, T, cache_seqlens, k, v)
+    strides = (T * Hkv * 128, Hkv * 128, 128, 1)
+    if k is None:
+        k = torch.empty_strided(shape, strides, dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty_strided(shape, strides, dtype=torch.bfloat16, device=dev)
+    _check("attn_kvq_read", lib.attn_kvq_read(*ptrs, None if cache_seqlens is None else cache_seqlens.data_ptr(),
+                                              k.data_ptr(), v.data_ptr(), B, T, Hkv, Tk, 128, bits, group,
+                                              _raw_stream(dev.index)))
+    return k, v
 
 
 @functools.lru_cache(maxsize=1024)
@@ -504,23 +527,21 @@ def attn_decode_kvq(q: torch.Tensor, cache, cache_seqlens: torch.Tensor, scale: 
         _check_f32("lse", lse, (B, H, Tq), dev)
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be contiguous and on {dev}, like every tensor of one call")
-    out, out_lse = o, lse
-
-    def call(handle):
-        nonlocal out, out_lse
-        out = torch.empty_like(q) if out is None else out
-        if out_lse is None:
-            out_lse = torch.empty_strided((B, H, Tq), (H * Tq, Tq, 1), dtype=torch.float32, device=dev)
-        ws = workspace
-        if ws is None:
-            need = _decode_kvq_workspace(B, H, Hkv, Tq, Tk, D)
-            ws = q.new_empty(need, dtype=torch.uint8) if need else None
-        ws_ptr, ws_bytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
-        return lib.attn_decode_kvq(q.data_ptr(), *ptrs, cache_seqlens.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
-                                   ws_ptr, ws_bytes, B, H, Hkv, Tq, Tk, D, bits, group, scale, win, handle)
-
-    _check("attn_decode_kvq", _launch(dev, stream, call))
-    return out, out_lse
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_decode_kvq(q, cache, cache_seqlens, scale, o, lse, workspace, window=window)
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty_strided((B, H, Tq), (H * Tq, Tq, 1), dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = _decode_kvq_workspace(B, H, Hkv, Tq, Tk, D)
+        workspace = q.new_empty(need, dtype=torch.uint8) if need else None
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _check("attn_decode_kvq", lib.attn_decode_kvq(q.data_ptr(), *ptrs, cache_seqlens.data_ptr(), o.data_ptr(),
+                                                  lse.data_ptr(), ws_ptr, ws_bytes, B, H, Hkv, Tq, Tk, D, bits, group,
+                                                  scale, win, _raw_stream(dev.index)))
+    return o, lse
 
 
 ROPE_PAIRINGS = {"interleaved": 0, "half": 1}

@@ -249,3 +249,22 @@ def test_lengths_are_checked():
                 torch.ones(2, dtype=torch.int32, device="meta")):
         with pytest.raises(ValueError):
             attn._check_seqlens(bad, 2, dev)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Before anything is changed: the current device and stream stay."""
+    class Other:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        with attn._on(torch.device("cuda", 0), Other()):
+            pass
+
+
+def test_what_is_no_cache_is_refused():
+    c = attn.kvq_cache(1, 1, 4, device="cpu")
+    for bad in (iter(c), dict(zip("abcd", c)), "abcd", [1, 2, 3, 4], torch.zeros(4, 1, 1, 4, 64, dtype=torch.uint8), None,
+                c[:3], (*c, c[0]), (*c[:3], c[3].to("meta")), (c[0], c[1][..., 0], c[2], c[3])):
+        with pytest.raises(ValueError, match="cache must|is on meta|k_params has shape"):
+            attn._check_kvq(bad)
+    assert attn._check_kvq(list(c))[1:6] == (1, 1, 4, 4, 64)
