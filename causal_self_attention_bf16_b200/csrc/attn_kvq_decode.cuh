@@ -591,12 +591,12 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       uint32_t vsz[2 * kN][kGroups];
 #pragma unroll
       for (int y = 0; y < 2 * kN; ++y) lds(vsz[y], ap + kp_lds + Shape::kParamBytes + 8 * y * kGroups * 4);
-      float top[kGroups];  // the largest scale of this lane's keys
+      float top[kGroups];  // the largest scale of this lane's keys (a cache filled by others may hold negative ones)
 #pragma unroll
       for (int j = 0; j < kGroups; ++j) {
-        top[j] = __uint_as_float(vsz[0][j] << 16);
+        top[j] = fabsf(__uint_as_float(vsz[0][j] << 16));
 #pragma unroll
-        for (int y = 1; y < 2 * kN; ++y) top[j] = fmaxf(top[j], __uint_as_float(vsz[y][j] << 16));
+        for (int y = 1; y < 2 * kN; ++y) top[j] = fmaxf(top[j], fabsf(__uint_as_float(vsz[y][j] << 16)));
         raise |= top[j] * unit[j] > 64.f;
       }
       if (__any_sync(0xffffffffu, raise)) {

@@ -225,9 +225,9 @@ def check_decode(q, cache, lens, scale, window, o, lse, what):
     for b, L in enumerate(min(max(L, 0), Tk) for L in lens):
         for h in range(H):
             k, v = (dequantize(t[b, h // G, :L].numpy(), p[b, h // G, :L], bits) for t, p in ((kc, kp), (vc, vp)))
-            ks, vs = (np.repeat(np.abs(cpu(p[b, h // G, :L, :, 1])) + c * cpu(p[b, h // G, :L, :, 0]),
+            ks, vs = (np.repeat(np.abs(cpu(p[b, h // G, :L, :, 1])) + c * np.abs(cpu(p[b, h // G, :L, :, 0])),
                                 D // p.shape[3], -1) for p in (kp, vp))
-            vstep = np.repeat(cpu(vp[b, h // G, :L, :, 0]), D // vp.shape[3], -1)
+            vstep = np.repeat(np.abs(cpu(vp[b, h // G, :L, :, 0])), D // vp.shape[3], -1)
             for i in range(Tq):
                 last = L - Tq + i
                 w = f"{what} b={b} h={h} i={i}"
@@ -414,6 +414,25 @@ def test_decode_extreme_scales():
         o, lse = attn.attn_decode_kvq(q, cache, ints([Tk]))
         clean()
         check_decode(q, cache, [Tk], 128 ** -0.5, None, o, lse, f"extreme scales {bits}")
+
+
+@pytest.mark.parametrize("bits,group", BITS_GROUPS)
+def test_decode_of_a_cache_filled_by_others(bits, group):
+    """Any codes and params are n * s + z: scales of both signs, all negative, and groups of sizes far apart."""
+    B, H, Hkv, Tq, Tk, lens = 3, 4, 2, 2, 200, [200, 37, 133]
+    cache = attn.kvq_cache(B, Hkv, Tk, bits, group)
+    g = torch.Generator(device="cuda").manual_seed(bits + group)
+    for codes, params in ((cache.k_codes, cache.k_params), (cache.v_codes, cache.v_params)):
+        codes.copy_(torch.randint(0, 256, codes.shape, generator=g, device="cuda", dtype=torch.uint8))
+        params.copy_(torch.randn(params.shape, generator=g, device="cuda") * 2.0 ** (1 - bits))
+    cache.k_params[1, ..., 0].abs_().neg_()
+    cache.v_params[1, ..., 0].abs_().neg_()
+    cache.v_params[2, :, 50:90] *= 2.0 ** 20
+    cache.v_params[2, :, 90:] *= -2.0 ** 40
+    q = randn((B, Tq, H, 128), 33).cuda()
+    o, lse = attn.attn_decode_kvq(q, cache, ints(lens))
+    clean()
+    check_decode(q, cache, lens, 128 ** -0.5, None, o, lse, f"by others {bits} {group}")
 
 
 def test_decode_is_repeatable_and_leaves_its_inputs():
