@@ -25,10 +25,12 @@
 //   so that the fp32 accumulators hold sums of both signs: they are cut off, not rounded (1 + 1.5 * 2^-24 stays 1),
 //   which sums of one sign over a whole cache would show. p_j s_g is the B fragment, rounded to fp16: 2^-11 of itself
 //   at most against the output's own 2^-8. So that it is in fp16's range whatever the scales, it is carried in units
-//   of a power of two per group of dims, raised when a key's scale passes it by 2^6 (and the sums rescaled). The
-//   second sum is fp32 throughout.
-//   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 8 (then p <= 2^8
-//   and the sums stay far from overflow): one vote a tile in place of the reduction and the rescaling.
+//   of a power of two per query row and group of dims, in which the largest so far is 1 or more (one below 2^-25 of
+//   that is lost). Per row, since a row must not lose its weights to the scale of a key that it does not see or hardly
+//   weighs (one unit for all rows was 0.5 % faster, 3 % in groups of 32). The second sum is fp32 throughout.
+//   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 4 (then p <= 2^4
+//   and the sums stay far from overflow) or a scale its unit by 2^11: one vote a tile in place of the reduction and
+//   the rescaling.
 //
 // Work split. A unit is one (sequence, key/value head); its visible keys, tiles of 32 (8 bits: 16). All units' tiles
 // in a row, with two places more for each unit's own cost, are dealt to the warps in equal stretches, found on the
@@ -290,6 +292,9 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   constexpr int kVWords = kGroup * kBits / 256;  // of a value row and group that a lane multiplies (0: half a word)
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
   constexpr float kNone = -3e38f;                // running max before the first key
+  // A score passes the running max by at most kLazy (log2) and |s| unit is at most kMostScale without a raise, so that
+  // a weight is at most 2^15, in fp16's range.
+  constexpr float kLazy = 4.f, kMostScale = 2048.f, kMostUnit = 0x1p100f;
   extern __shared__ __align__(128) uint8_t kvq_smem[];
   __shared__ KvqPiece sh_piece[2 * kKvqWarps];  // stretch i's slots at 2 i, 2 i + 1
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
@@ -518,11 +523,11 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       down[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
     float acc[8][4], corr[kGroups][2], m[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
-    float unit[kGroups];  // value weights are in units of 1 / unit, a power of two
+    float unit[kGroups][2];  // the weights p s of columns 2 t, 2 t + 1 are in units of 1 / unit, a power of two
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = 0.f, unit[j] = 0x1p126f;
+    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = 0.f, unit[j][0] = unit[j][1] = kMostUnit;
 
     // The tile of codes at `at` and params at `ap`: n_halves times 16 keys, from key0 on.
     auto tile = [&](const uint32_t at, const uint32_t ap, const int key0, auto masked, auto n_halves) {
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
       for (int e = 0; e < 4 * kN; ++e) {
         x[e] = seen[e] ? fmaf(s[e], down[e & 1], -m[e & 1]) : -INFINITY;
-        raise |= x[e] > 8.f;
+        raise |= x[e] > kLazy;
       }
       uint32_t vsz[2 * kN][kGroups];
 #pragma unroll
@@ -597,9 +602,12 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         top[j] = fabsf(__uint_as_float(vsz[0][j] << 16));
 #pragma unroll
         for (int y = 1; y < 2 * kN; ++y) top[j] = fmaxf(top[j], fabsf(__uint_as_float(vsz[y][j] << 16)));
-        raise |= top[j] * unit[j] > 64.f;
+        raise |= top[j] * unit[j][0] > kMostScale || top[j] * unit[j][1] > kMostScale;
       }
       if (__any_sync(0xffffffffu, raise)) {
+        // A column's max becomes a whole number, so that the old weights' factor is a power of two, which their sums
+        // in acc take up as their unit's.
+        int up[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float y = m[c];  // the new max
@@ -608,6 +616,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
             if (seen[e]) y = fmaxf(y, s[e] * down[c]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+          y = ceilf(y);
+          up[c] = static_cast<int>(fminf(y - m[c], 1000.f));
           const float f = ex2(m[c] - y);
           m[c] = y;
 #pragma unroll
@@ -615,23 +625,29 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
             if (seen[e]) x[e] = fmaf(s[e], down[c], -y);
           l[c] *= f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i][c] *= f, acc[i][c + 2] *= f;
-#pragma unroll
           for (int j = 0; j < kGroups; ++j) corr[j][c] *= f;
         }
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
-          float y = top[j];
+          uint32_t most = 0;  // the tile's largest p |s|, the upper half of the fp32 number: column 2 t, 2 t + 1
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-          if (y * unit[j] > 64.f) {  // the unit becomes the largest scale's power of two
-            const int e = static_cast<int>(__float_as_uint(y) >> 23);  // its exponent field
-            const float to = __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 1), 253)) << 23);
-            const float f = to * kvq_inverse(unit[j]);
-            unit[j] = to;
+          for (int y = 0; y < 2 * kN; ++y) {
+            const float sc = fabsf(__uint_as_float(vsz[y][j] << 16));
+            const float w0 = seen[2 * y] ? ex2(x[2 * y]) * sc : 0.f, w1 = seen[2 * y + 1] ? ex2(x[2 * y + 1]) * sc : 0.f;
+            most = __vmaxu2(most, __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632));
+          }
 #pragma unroll
-            for (int i = j * (kGroup / 16); i < (j + 1) * (kGroup / 16); ++i)
-              acc[i][0] *= f, acc[i][1] *= f, acc[i][2] *= f, acc[i][3] *= f;
+          for (int o = 4; o < 32; o <<= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, o));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            // in exponent fields: the unit that the sums have now, and the one from here on, with which the largest
+            // weight is below 2
+            const int at = static_cast<int>(__float_as_uint(unit[j][c]) >> 23) + up[c];
+            const int to = max(min(min(at, 127 + 100), 2 * 127 - static_cast<int>((most >> (16 * c + 7)) & 0xffu)), 1);
+            unit[j][c] = __uint_as_float(static_cast<uint32_t>(to) << 23);
+            const float f = to - at < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + to - at) << 23);
+#pragma unroll
+            for (int i = j * (kGroup / 16); i < (j + 1) * (kGroup / 16); ++i) acc[i][c] *= f, acc[i][c + 2] *= f;
           }
         }
       }
@@ -651,8 +667,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
             const int e = 4 * y + 2 * z;
             const uint32_t w = vsz[2 * y + z][j];
             const float sc = __uint_as_float(w << 16), zc = fmaf(kCentre, sc, __uint_as_float(w & 0xffff0000u));
-            const float su = sc * unit[j];
-            float w0 = x[e] * su, w1 = x[e + 1] * su;
+            float w0 = x[e] * unit[j][0] * sc, w1 = x[e + 1] * unit[j][1] * sc;
             if constexpr (masked.value) {  // (a NaN in a key that a row does not see stays out of it)
               if (!seen[e]) w0 = 0.f;
               if (!seen[e + 1]) w1 = 0.f;
@@ -724,9 +739,6 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         for (int j = 0; j < kGroups; ++j) corr[j][c] += __shfl_xor_sync(0xffffffffu, corr[j][c], o);
       }
     }
-    float worth[kGroups];  // 2^24 of the codes, and what a weight's unit is
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j) worth[j] = 0x1p24f * kvq_inverse(unit[j]);
     constexpr float kSecond = kBits == 4 ? 0.0625f : 1.f;  // rows g + 8 of a tile: second (fourth) nibbles
     if (!whole && slot) __syncwarp();  // (every lane has read the last tile, which the piece overwrites)
     float* to_o = piece_o(slot, warp);
@@ -740,8 +752,9 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const int j = x / (kGroup / 16), dim = j * kGroup + g * (kGroup / 8) + 2 * (x % (kGroup / 16));
-        const float a = fmaf(acc[x][c], worth[j], corr[j][c]);
-        const float b = fmaf(acc[x][c + 2] * kSecond, worth[j], corr[j][c]);
+        const float worth = 0x1p24f * kvq_inverse(unit[j][c]);  // 2^24 of the codes, and what a weight's unit is
+        const float a = fmaf(acc[x][c], worth, corr[j][c]);
+        const float b = fmaf(acc[x][c + 2] * kSecond, worth, corr[j][c]);
         if (!whole)
           *reinterpret_cast<float2*>(to_o + (2 * t + c) * 128 + dim) = make_float2(a, b);
         else if (ATTN_IN_RANGE(off + dim, 2, n_q, kSiteKvqDecO, &g_kvq_error))

@@ -14,6 +14,8 @@ Tolerances, derived from the arithmetic:
   o       : one bf16 rounding, 2^-8 |o|; each weight is off by 2 dS + 2^-14 of itself (exp2 and the running sums in
             fp32), counted against sum_j p_j (|z| + c s); and the product of a weight and a scale is rounded to fp16,
             2^-11 of itself, before it multiplies a code, centred or not, of at most 2^bits: 2^-11 sum_j p_j 2^bits s.
+            (One below 2^-14 of the largest of its row and group is off by up to 2^-25 of that largest: of 2^12 keys
+            together within the 2^-14 sum_j p_j 2 * 2^bits s above.)
 """
 import numpy as np
 import pytest
@@ -433,6 +435,28 @@ def test_decode_of_a_cache_filled_by_others(bits, group):
     o, lse = attn.attn_decode_kvq(q, cache, ints(lens))
     clean()
     check_decode(q, cache, lens, 128 ** -0.5, None, o, lse, f"by others {bits} {group}")
+
+
+@pytest.mark.parametrize("bits,group", BITS_GROUPS)
+def test_decode_values_of_other_sizes_where_they_do_not_count(bits, group):
+    """Values of very different sizes: at a key that only some rows see, at one that some rows hardly weigh, and at keys
+    that later ones leave far behind. Each row's result holds to its own weights."""
+    B, H, Hkv, Tq, Tk, lens = 3, 4, 2, 2, 300, [300, 290, 300]
+    cache = filled(B, Hkv, Tk, bits, group, lens, 140)
+    cache.v_params[0, :, 299] *= 2.0 ** 40               # the newest key: token 0 does not see it
+    cache.v_params[1, :, 7] *= 2.0 ** 30                 # heads 0 and 2 weigh it by about 2^-100, the others like any
+    q = randn((B, Tq, H, 128), 142).cuda()
+    q[1, :, 0::2], q[1, :, 1::2] = 1, 0
+    cache.k_params[1, :, 7, :, 0], cache.k_params[1, :, 7, :, 1] = 0, -6
+    cache.k_params[1, 1, 8:280, :, 1] += 0.01
+    q[2] = 1                                             # scores that rise by about 2^100 from end to end
+    cache.k_params[2, ..., 0] *= 0.01
+    cache.k_params[2, ..., 1] = torch.linspace(-3, 3, Tk, device="cuda")[None, :, None]
+    cache.v_params[2, 0, :40] *= 2.0 ** 40
+    cache.v_params[2, 1, 100] *= -2.0 ** 24
+    o, lse = attn.attn_decode_kvq(q, cache, ints(lens))
+    clean()
+    check_decode(q, cache, lens, 128 ** -0.5, None, o, lse, f"sizes {bits} {group}")
 
 
 def test_decode_is_repeatable_and_leaves_its_inputs():
