@@ -194,21 +194,23 @@ __global__ void __launch_bounds__(kWriteThreads) kvq_write_kernel(const CopyPara
   (void)n_new, (void)n_cache;
   const bool live = r < rows;  // (every lane stays for the shuffles)
   const CopyRow at = copy_row(p, live ? r : 0u);
+  // A warp whose tokens have no position reads nothing: half of a batch of left-padded prompts may be such (59 us
+  // against 81 for 32 prompts of up to 2,048 tokens; with none of them loads that wait for the lengths cost 4 %).
+  if (!__any_sync(0xffffffffu, live && at.there)) return;
   const size_t from = at.dense * size_t{128} + 16 * c;
-  uint32_t raw[2][8] = {};
-  if (live && ATTN_IN_RANGE(from, 16, n_new, kSiteKvqNew, &g_kvq_error)) {
+  const bool in = ATTN_IN_RANGE(from, 16, n_new, kSiteKvqNew, &g_kvq_error);
+  uint32_t raw[2][8];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {  // (read whether the token has a position or not: that is not known yet)
+  for (int t = 0; t < 2; ++t) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 u = reinterpret_cast<const uint4*>(p.x[t] + from)[i];
-        raw[t][4 * i] = u.x, raw[t][4 * i + 1] = u.y, raw[t][4 * i + 2] = u.z, raw[t][4 * i + 3] = u.w;
-      }
+    for (int i = 0; i < 2; ++i) {
+      const uint4 u = in ? reinterpret_cast<const uint4*>(p.x[t] + from)[i] : make_uint4(0u, 0u, 0u, 0u);
+      raw[t][4 * i] = u.x, raw[t][4 * i + 1] = u.y, raw[t][4 * i + 2] = u.z, raw[t][4 * i + 3] = u.w;
     }
   }
   const size_t to = at.cache * static_cast<size_t>(kRowBytes) + c * (2 * kBits);
   const size_t sz_to = at.cache * static_cast<size_t>(kGroups) + 16 * c / kGroup;
-  const bool write = live && at.there &&
+  const bool write = live && at.there && in &&
                      ATTN_IN_RANGE(to, 2 * kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error) &&
                      ATTN_IN_RANGE(sz_to, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error);
 #pragma unroll
