@@ -35,6 +35,10 @@ using attn::g_cuda_error;
 // read 12 to 38 % slower.
 constexpr int kReadThreads = 256, kWriteThreads = 128;
 constexpr int kReadLanes = 16, kWriteLanes = 8;  // threads per row
+// Blocks of write, at most: six times the nine that an SM holds. Blocks with one set of rows each were slower in
+// batches of padded prompts, where many have nothing to do (32 prompts of up to 2,048 tokens: 56 us against 49), and a
+// single wave of them in full ones (104 us against 86).
+constexpr unsigned kWriteBlocks = 148 * 54;
 enum : uint32_t {
   kSiteKvqNew = 0xa0, kSiteKvqCodes = 0xa1, kSiteKvqParams = 0xa2, kSiteKvqOut = 0xa3
 };
@@ -188,39 +192,42 @@ __global__ void __launch_bounds__(kWriteThreads) kvq_write_kernel(const CopyPara
   begin_early();
   constexpr int kRowBytes = 16 * kBits, kGroups = 128 / kGroup;
   const uint32_t c = threadIdx.x % kWriteLanes;
-  const uint32_t r = blockIdx.x * (kWriteThreads / kWriteLanes) + threadIdx.x / kWriteLanes;
+  constexpr uint32_t kRows = kWriteThreads / kWriteLanes;
   const uint32_t rows = static_cast<uint32_t>(p.B) * p.T * p.Hkv;
   const size_t n_new = static_cast<size_t>(rows) * 128, n_cache = static_cast<size_t>(p.B) * p.Hkv * p.Tk;
   (void)n_new, (void)n_cache;
-  const bool live = r < rows;  // (every lane stays for the shuffles)
-  const CopyRow at = copy_row(p, live ? r : 0u);
-  // A warp whose tokens have no position reads nothing: half of a batch of left-padded prompts may be such (59 us
-  // against 81 for 32 prompts of up to 2,048 tokens; with none of them loads that wait for the lengths cost 4 %).
-  if (!__any_sync(0xffffffffu, live && at.there)) return;
-  const size_t from = at.dense * size_t{128} + 16 * c;
-  const bool in = ATTN_IN_RANGE(from, 16, n_new, kSiteKvqNew, &g_kvq_error);
-  uint32_t raw[2][8];
+  for (uint32_t r0 = blockIdx.x * kRows; r0 < rows; r0 += gridDim.x * kRows) {
+    const uint32_t r = r0 + threadIdx.x / kWriteLanes;
+    const bool live = r < rows;  // (every lane stays for the shuffles)
+    const CopyRow at = copy_row(p, live ? r : 0u);
+    // A warp whose tokens have no position reads nothing: half of a batch of left-padded prompts may be such (59 us
+    // against 81 for 32 prompts of up to 2,048 tokens; with none of them loads that wait for the lengths cost 4 %).
+    if (!__any_sync(0xffffffffu, live && at.there)) continue;
+    const size_t from = at.dense * size_t{128} + 16 * c;
+    const bool in = ATTN_IN_RANGE(from, 16, n_new, kSiteKvqNew, &g_kvq_error);
+    uint32_t raw[2][8];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 2; ++t) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 u = in ? reinterpret_cast<const uint4*>(p.x[t] + from)[i] : make_uint4(0u, 0u, 0u, 0u);
-      raw[t][4 * i] = u.x, raw[t][4 * i + 1] = u.y, raw[t][4 * i + 2] = u.z, raw[t][4 * i + 3] = u.w;
+      for (int i = 0; i < 2; ++i) {
+        const uint4 u = in ? reinterpret_cast<const uint4*>(p.x[t] + from)[i] : make_uint4(0u, 0u, 0u, 0u);
+        raw[t][4 * i] = u.x, raw[t][4 * i + 1] = u.y, raw[t][4 * i + 2] = u.z, raw[t][4 * i + 3] = u.w;
+      }
     }
-  }
-  const size_t to = at.cache * static_cast<size_t>(kRowBytes) + c * (2 * kBits);
-  const size_t sz_to = at.cache * static_cast<size_t>(kGroups) + 16 * c / kGroup;
-  const bool write = live && at.there && in &&
-                     ATTN_IN_RANGE(to, 2 * kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error) &&
-                     ATTN_IN_RANGE(sz_to, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error);
+    const size_t to = at.cache * static_cast<size_t>(kRowBytes) + c * (2 * kBits);
+    const size_t sz_to = at.cache * static_cast<size_t>(kGroups) + 16 * c / kGroup;
+    const bool write = live && at.there && in &&
+                       ATTN_IN_RANGE(to, 2 * kBits, n_cache * kRowBytes, kSiteKvqCodes, &g_kvq_error) &&
+                       ATTN_IN_RANGE(sz_to, 1, n_cache * kGroups, kSiteKvqParams, &g_kvq_error);
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    uint32_t sz, codes[kBits / 2];
-    quantise16<kBits, kGroup>(raw[t], codes, &sz);
-    if (!write) continue;
-    if constexpr (kBits == 4) *reinterpret_cast<uint2*>(p.codes[t] + to) = make_uint2(codes[0], codes[1]);
-    else *reinterpret_cast<uint4*>(p.codes[t] + to) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-    if ((16 * c) % kGroup == 0) p.params[t][sz_to] = sz;
+    for (int t = 0; t < 2; ++t) {
+      uint32_t sz, codes[kBits / 2];
+      quantise16<kBits, kGroup>(raw[t], codes, &sz);
+      if (!write) continue;
+      if constexpr (kBits == 4) *reinterpret_cast<uint2*>(p.codes[t] + to) = make_uint2(codes[0], codes[1]);
+      else *reinterpret_cast<uint4*>(p.codes[t] + to) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+      if ((16 * c) % kGroup == 0) p.params[t][sz_to] = sz;
+    }
   }
 }
 
@@ -357,7 +364,8 @@ cudaError_t launch_early(void (*kernel)(P), dim3 grid, int threads, size_t smem,
 attn_status launch_copy(bool write, const CopyParams& p, int bits, int group, void* stream) {
   const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv;
   const int threads = write ? kWriteThreads : kReadThreads, per_block = threads / (write ? kWriteLanes : kReadLanes);
-  const unsigned grid = static_cast<unsigned>((rows + per_block - 1) / per_block);
+  unsigned grid = static_cast<unsigned>((rows + per_block - 1) / per_block);
+  if (write) grid = std::min(grid, kWriteBlocks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   with_format(bits, group, [&](auto b, auto g) {

@@ -147,19 +147,21 @@ def test_write_codes_are_the_formula_bit_for_bit(bits, group):
     assert torch.equal(cache.k_params[0, 0].cpu().float(), torch.cat([s, z], -1))
 
 
-def test_write_many_rows():
-    """Enough rows for many blocks, checked against the oracle on a sample and for every row's error bound."""
-    B, T, Hkv, bits, group = 3, 701, 10, 4, 64
+@pytest.mark.parametrize("T", [701, 4503])
+def test_write_many_rows(T):
+    """Enough rows for many blocks (T = 4503: for some that take several sets of rows), checked against the oracle on a
+    sample and for every row's error bound."""
+    B, Hkv, bits, group, lens = 3, 10, 4, 64, (T, T + 99, T + 199)
     k, v = randn((B, T, Hkv, 128), 5).cuda(), randn((B, T, Hkv, 128), 6).cuda()
-    cache = attn.kvq_cache(B, Hkv, 900, bits, group)
-    attn.kvq_write(cache, k, v, ints([701, 800, 900]))
-    rk, rv = attn.kvq_read(cache, T, ints([701, 800, 900]))
+    cache = attn.kvq_cache(B, Hkv, T + 199, bits, group)
+    attn.kvq_write(cache, k, v, ints(lens))
+    rk, rv = attn.kvq_read(cache, T, ints(lens))
     clean()
-    for b, L in enumerate((701, 800, 900)):
+    for b, L in enumerate(lens):
         for h in (0, 7):
             check_row(k[b, :, h].cpu(), cache.k_codes[b, h, L - T:L], cache.k_params[b, h, L - T:L], bits, group, "k")
     for x, y, p in ((k, rk, cache.k_params), (v, rv, cache.v_params)):
-        step = torch.stack([p[b, :, L - T:L, :, 0] for b, L in enumerate((701, 800, 900))]).transpose(1, 2).float()
+        step = torch.stack([p[b, :, L - T:L, :, 0] for b, L in enumerate(lens)]).transpose(1, 2).float()
         bound = step.repeat_interleave(group, -1) / 2 + 2.0 ** -7 * x.float().abs() + 2.0 ** -8 * step.amax(-1, True)
         assert ((x.float() - y.float()).abs() <= bound).all()
 
