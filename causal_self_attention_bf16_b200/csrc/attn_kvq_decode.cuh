@@ -17,17 +17,18 @@
 //   Scores. For key j and query row r, with the sums taken group by group of dims:
 //     q . k = sum_g s_g (sum_d q_d n_d) + z_g (sum_d q_d).     The first sum is the matrix product, the last is made
 //   once per query row. A query row is scaled by a power of two that puts its largest dim into [2^14, 2^15), so that
-//   its bf16 numbers are fp16 numbers (exactly down to 2^-34 of the largest); the power goes off with the softmax
-//   scale. The unit aligns products by their factors' exponent fields, so a subnormal factor's leading zeros are bits
-//   that small products of a sum lose: with the codes lse stays within 5e-7 of itself, but the queries' sums, whose
-//   other factor could be as small as 2^-24, are made with 1 (lse was off by 2e-6 otherwise).
+//   its bf16 numbers are fp16 numbers (exactly down to 2^-27 of the largest, below that to 2^-35 of it); the power
+//   goes off with the softmax scale. The unit aligns products by their factors' exponent fields, so a subnormal
+//   factor's leading zeros are bits that small products of a sum lose: with the codes lse stays within 5e-7 of
+//   itself, but the queries' sums, whose other factor could be as small as 2^-24, are made with 1 (lse was off by
+//   2e-6 otherwise).
 //   Values. o = sum_j p_j s_g (n - c) + sum_j p_j (z_g + c s_g), c = 8 or 128: one packed addition centres the codes,
 //   so that the fp32 accumulators hold sums of both signs: they are cut off, not rounded (1 + 1.5 * 2^-24 stays 1),
 //   which sums of one sign over a whole cache would show. p_j s_g is the B fragment, rounded to fp16: 2^-11 of itself
 //   at most against the output's own 2^-8. So that it is in fp16's range whatever the scales, it is carried in units
 //   of a power of two per query row and group of dims, in which the largest so far is 1 or more (one below 2^-25 of
-//   that is lost). Per row, since a row must not lose its weights to the scale of a key that it does not see or hardly
-//   weighs (one unit for all rows was 0.5 % faster, 3 % in groups of 32). The second sum is fp32 throughout.
+//   that is lost). Per row, since a row must not lose its weights to the scale of a key that it does not see or
+//   hardly weighs (one unit for all rows was 0.5 % faster, 3 % in groups of 32). The second sum is fp32 throughout.
 //   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 4 (then p <= 2^4
 //   and the sums stay far from overflow) or a scale its unit by 2^11: one vote a tile in place of the reduction and
 //   the rescaling.
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   // --- the ring
   const uint32_t ring = sm100::smem_u32(kvq_smem) + warp * kStages * Shape::kStageBytes;
   constexpr int kChunks = kRowBytes / 16, kRowsAtOnce = 32 / kChunks;  // 16-byte chunks of a row; rows a copy covers
-  const int c_row = lane / kChunks, p_row = lane % 16;  // (params: key rows by the lower lanes, value rows by the upper)
+  const int c_row = lane / kChunks, p_row = lane % 16;  // (params: key rows by the lower lanes, else value rows)
   // (a copy's rows are a multiple of 4 apart, and of 8 where the swizzle looks at bit 2)
   uint32_t code_at[kTile / kRowsAtOnce];
 #pragma unroll
@@ -633,7 +634,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
           for (int y = 0; y < 2 * kN; ++y) {
             const float sc = fabsf(__uint_as_float(vsz[y][j] << 16));
-            const float w0 = seen[2 * y] ? ex2(x[2 * y]) * sc : 0.f, w1 = seen[2 * y + 1] ? ex2(x[2 * y + 1]) * sc : 0.f;
+            const float w0 = seen[2 * y] ? ex2(x[2 * y]) * sc : 0.f;
+            const float w1 = seen[2 * y + 1] ? ex2(x[2 * y + 1]) * sc : 0.f;
             most = __vmaxu2(most, __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632));
           }
 #pragma unroll
