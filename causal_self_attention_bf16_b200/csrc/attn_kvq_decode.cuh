@@ -754,9 +754,10 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const int j = x / (kGroup / 16), dim = j * kGroup + g * (kGroup / 8) + 2 * (x % (kGroup / 16));
-        const float worth = 0x1p24f * kvq_inverse(unit[j][c]);  // 2^24 of the codes, and what a weight's unit is
-        const float a = fmaf(acc[x][c], worth, corr[j][c]);
-        const float b = fmaf(acc[x][c + 2] * kSecond, worth, corr[j][c]);
+        // 2^24 of the codes, then what a weight's unit is: their product may pass fp32's range where the result does not
+        const float inverse = kvq_inverse(unit[j][c]);
+        const float a = fmaf(acc[x][c] * 0x1p24f, inverse, corr[j][c]);
+        const float b = fmaf(acc[x][c + 2] * (0x1p24f * kSecond), inverse, corr[j][c]);
         if (!whole)
           *reinterpret_cast<float2*>(to_o + (2 * t + c) * 128 + dim) = make_float2(a, b);
         else if (ATTN_IN_RANGE(off + dim, 2, n_q, kSiteKvqDecO, &g_kvq_error))
