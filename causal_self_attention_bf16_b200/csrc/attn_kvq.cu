@@ -25,7 +25,12 @@
 #include "attn_errors.h"
 #include "attn_kvq_decode.cuh"
 
+using attn::add2;
+using attn::F2;
+using attn::f2;
+using attn::fma2;
 using attn::g_kvq_error;
+using attn::mul2;
 
 namespace {
 
@@ -87,31 +92,6 @@ __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinter
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// Two fp32 operations in one instruction, each rounded to nearest.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 
 // Quantise this thread's 16 dims (bf16 pairs w), in a group that spans kGroup / 16 neighbouring threads: their codes,
 // packed in dim order, and the group's (s, z) word.

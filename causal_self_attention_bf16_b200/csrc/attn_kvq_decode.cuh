@@ -156,6 +156,33 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   return c;
 }
 
+// Two fp32 operations in one instruction, each rounded to nearest.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float lo_of(F2 a) { return __uint_as_float(static_cast<uint32_t>(a.v)); }
+__device__ __forceinline__ float hi_of(F2 a) { return __uint_as_float(static_cast<uint32_t>(a.v >> 32)); }
+
 // Nibbles 0..3 of the low and of the high half of w as fp16 numbers n * 2^-24 (x[0], x[2]) and n * 2^-20 (x[1], x[3]);
 // centred: n - 8.
 template <bool kCentred>
@@ -587,12 +614,16 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
           seen[e] = key <= hi && (p.window < 0 || key >= hi - p.window);
         }
       }
+      // In log2 units a score is rounded before the max, one of them, comes off: the largest one then weighs 1 however
+      // large it is. (An unrounded product less the max left it half a unit in the last place, 2^7 at 2^31.)
       float x[4 * kN];  // log2 of the weights
       bool raise = false;
 #pragma unroll
-      for (int e = 0; e < 4 * kN; ++e) {
-        x[e] = seen[e] ? fmaf(s[e], down[e & 1], -m[e & 1]) : -INFINITY;
-        raise |= x[e] > kLazy;
+      for (int e = 0; e < 4 * kN; e += 2) {
+        const F2 score = mul2(f2(s[e], s[e + 1]), f2(down[0], down[1])), less = add2(score, f2(-m[0], -m[1]));
+        s[e] = lo_of(score), s[e + 1] = hi_of(score);
+        x[e] = seen[e] ? lo_of(less) : -INFINITY, x[e + 1] = seen[e + 1] ? hi_of(less) : -INFINITY;
+        raise |= x[e] > kLazy || x[e + 1] > kLazy;
       }
       uint32_t vsz[2 * kN][kGroups];
 #pragma unroll
@@ -614,7 +645,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
           float y = m[c];  // the new max
 #pragma unroll
           for (int e = c; e < 4 * kN; e += 2)
-            if (seen[e]) y = fmaxf(y, s[e] * down[c]);
+            if (seen[e]) y = fmaxf(y, s[e]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
           y = ceilf(y);
@@ -623,7 +654,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
           m[c] = y;
 #pragma unroll
           for (int e = c; e < 4 * kN; e += 2)
-            if (seen[e]) x[e] = fmaf(s[e], down[c], -y);
+            if (seen[e]) x[e] = s[e] - y;
           l[c] *= f;
 #pragma unroll
           for (int j = 0; j < kGroups; ++j) corr[j][c] *= f;

@@ -32,3 +32,40 @@ def test_huge_values(bits, group, size, Tk):
     are divided (weights of at most 2^4, 1 where the keys are one tile's) stay below fp32's largest number."""
     k, v = randn((2, Tk, 2, 128), 1, 0.2), randn((2, Tk, 2, 128), 2, 0.0).float() * size
     decode_of(k, v, randn((2, 1, 4, 128), 3, 0.2), bits, group, [Tk, Tk // 2])
+
+
+@pytest.mark.parametrize("size", [2.0 ** 20, 1e10, 1e25, 1e35])
+@pytest.mark.parametrize("Tk,Tq", [(20, 1), (700, 3), (6000, 1)])
+@pytest.mark.parametrize("bits,group", [(4, 64), (8, 32)])
+def test_huge_scores(bits, group, Tk, Tq, size):
+    """Scores far past 2^24: of each row's keys the largest one takes all the weight, or those that tie for it do in
+    equal parts. A row's scores are its size times the first dim's code, so they are known: lse is the largest and the
+    logarithm of how many have it (the rounding of the score and of the base-2 scale: under 2^-20 together), o the mean
+    of their values (2^-8 of itself for bf16, 2^-11 * 2^bits * s for the weights)."""
+    B, H, Hkv = 2, 6, 2
+    g = torch.Generator().manual_seed(bits + Tk)
+    cache = attn.kvq_cache(B, Hkv, Tk, bits, group)
+    attn.kvq_write(cache, torch.zeros(B, Tk, Hkv, 128, dtype=torch.bfloat16, device="cuda"),
+                   randn((B, Tk, Hkv, 128), 5, 0.0).cuda(), ints([Tk] * B))
+    n = torch.randint(0, 15, (B, Hkv, Tk), generator=g)
+    for at in ((Tk - Tq) // 3, (Tk - Tq) // 2, Tk - Tq):          # seen by every query: the largest, three times
+        n[:, :, at] = 15
+    cache.k_codes[..., 0] = n.to(torch.uint8).cuda()              # (4 bits: dim 1's code, the high half, is 0)
+    cache.k_params[..., 0] = 1
+    q = torch.zeros(B, Tq, H, 128)
+    q[..., 0] = size * torch.linspace(0.7, 1.3, H)
+    q = q.to(torch.bfloat16).cuda()
+    o, lse = attn.attn_decode_kvq(q, cache, ints([Tk] * B), 0.0883)
+    clean()
+    top = 15 * np.float64(np.float32(0.0883)) * cpu(q)[..., 0].transpose(0, 2, 1)
+    assert (np.abs(cpu(lse) - top - np.log(3)) <= 2.0 ** -20 * top + 2.0 ** -20).all()
+    codes = (cache.v_codes[..., None] >> torch.tensor([0, 4], device="cuda") & 15).flatten(-2) if bits == 4 else cache.v_codes
+    step = cpu(cache.v_params[..., 0].repeat_interleave(group, -1))
+    values = cpu(codes) * step + cpu(cache.v_params[..., 1].repeat_interleave(group, -1))
+    for b in range(B):
+        for h in range(Hkv):
+            keys = (n[b, h] == 15).numpy()
+            mean = values[b, h, keys].mean(0)
+            size_of = (np.abs(values[b, h, keys]) + 2 * 2 ** bits * step[b, h, keys]).mean(0)
+            tol = 2.0 ** -8 * np.abs(mean) + (2.0 ** -11 + 2.0 ** -14) * size_of
+            assert (np.abs(cpu(o)[b, :, 3 * h:3 * h + 3] - mean) <= tol).all()
