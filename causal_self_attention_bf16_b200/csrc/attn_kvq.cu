@@ -528,7 +528,7 @@ attn_status attn_decode_kvq(const void* q, const void* k_codes, const void* k_pa
   p.lse = lse;
   p.B = B, p.H = H, p.Hkv = H_kv, p.Tq = Tq, p.Tk = Tk;
   p.window = window < Tk ? window : -1;  // (a window of the capacity hides nothing)
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.half_scale_log2 = scale * (0.5f * 1.4426950408889634f);
   const int R = p.R = (H / H_kv) * Tq;
   for (int r = 0; r < attn::kKvqMaxRows; ++r) p.row_i[r] = r < R ? r % Tq : 0, p.row_g[r] = r < R ? r / Tq : 0;
   const DecodeSplit split = decode_split(B, H, H_kv, Tq, decode_span(Tq, Tk, window));

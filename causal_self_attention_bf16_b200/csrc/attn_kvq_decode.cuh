@@ -97,7 +97,7 @@ struct KvqDecodeParams {
   int B, H, Hkv, Tq, Tk, R;
   int window;                    // sliding window: the query at position p sees keys p - window .. p; -1: none
   int whole;                     // 1: every CTA has whole units (at most 32 of them): no piece is left to merge
-  float scale_log2;              // scale * log2(e)
+  float half_scale_log2;         // scale * log2(e) / 2 (finite for any finite scale)
   double per_stretch;            // 1 / the warps' stretches of the row of all places (of the CTA's with `whole`)
   uint8_t row_i[kKvqMaxRows], row_g[kKvqMaxRows];  // row r is token r % Tq of query head r / Tq of the group
 };
@@ -238,6 +238,8 @@ __device__ __forceinline__ void lds(uint32_t (&w)[kWords], uint32_t addr) {
   }
 }
 
+// 2^e of e in [-126, 127].
+__device__ __forceinline__ float kvq_power(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 // 1 / x of a power of two in [2^-126, 2^126].
 __device__ __forceinline__ float kvq_inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
@@ -320,6 +322,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   constexpr int kVWords = kGroup * kBits / 256;  // of a value row and group that a lane multiplies (0: half a word)
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
   constexpr float kNone = -3e38f;                // running max before the first key
+  constexpr float kMost = 3.402823466e38f;       // fp32's largest number
+  constexpr int kLift = 120;
   // A score passes the running max by at most kLazy (log2) and |s| unit is at most kMostScale without a raise, so that
   // a weight is at most 2^15, in fp16's range.
   constexpr float kLazy = 4.f, kMostScale = 2048.f, kMostUnit = 0x1p100f;
@@ -499,7 +503,9 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
     // as their codes are 2^4 larger).
     uint32_t qb[16];
     float qsum[kGroups][2];  // a group's sum of q over its dims, units of 2^(24 - up), of columns 2 t and 2 t + 1
-    float down[2];           // softmax scale (log2 units) times 2^(24 - up) of columns 2 t and 2 t + 1
+    // softmax scale (log2 units) times 2^(24 - up) of columns 2 t and 2 t + 1; where that is past fp32's range (queries
+    // of 2^121 or more at the default scale, whose scores tiny keys may bring back into it), less 2^kLift, and negative
+    float down[2];
     {
       const int row = rt * 8 + g, i = p.row_i[row], h = cur.hk * G + p.row_g[row];
       const size_t off = ((static_cast<size_t>(cur.b) * p.Tq + i) * p.H + h) * 128;
@@ -546,10 +552,15 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         mma_16x8x16(qs[j], kOne, kOne, kSecond, kSecond, qb[4 * x + 2], qb[4 * x + 3]);
         qsum[j][0] = qs[j][0] * 0x1p-24f, qsum[j][1] = qs[j][1] * 0x1p-24f;
       }
-      const float back = (p.scale_log2 * 0x1p24f) * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+      const int e = 25 - up;  // in [-101, 139]
+      float back = p.half_scale_log2 * kvq_power(min(e, 127)) * kvq_power(max(e - 127, 0));
+      if (back == INFINITY) back = -fminf(p.half_scale_log2 * kvq_power(-kLift / 2) * kvq_power(e - kLift / 2), kMost);
       down[0] = __shfl_sync(0xffffffffu, back, 8 * t);
       down[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
+    // the last tile that needs no mask begins here, if any (none where a score has two factors: those are the masked
+    // tiles', so that the others do without; a flag of its own was 1 % slower)
+    const int plain_to = __any_sync(0xffffffffu, down[0] < 0.f || down[1] < 0.f) ? -1 : cur.s.L - p.Tq - (kTile - 1);
     float acc[8][4], corr[kGroups][2], m[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
     float unit[kGroups][2];  // the weights p s of columns 2 t, 2 t + 1 are in units of 1 / unit, a power of two
 #pragma unroll
@@ -620,7 +631,13 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       bool raise = false;
 #pragma unroll
       for (int e = 0; e < 4 * kN; e += 2) {
-        const F2 score = mul2(f2(s[e], s[e + 1]), f2(down[0], down[1])), less = add2(score, f2(-m[0], -m[1]));
+        F2 score = f2(s[e], s[e + 1]), factor = f2(down[0], down[1]);
+        if constexpr (masked.value) {
+          score = mul2(score, f2(down[0] < 0.f ? kvq_power(kLift) : 1.f, down[1] < 0.f ? kvq_power(kLift) : 1.f));
+          factor = f2(fabsf(down[0]), fabsf(down[1]));
+        }
+        score = mul2(score, factor);
+        const F2 less = add2(score, f2(-m[0], -m[1]));
         s[e] = lo_of(score), s[e + 1] = hi_of(score);
         x[e] = seen[e] ? lo_of(less) : -INFINITY, x[e + 1] = seen[e + 1] ? hi_of(less) : -INFINITY;
         raise |= x[e] > kLazy || x[e + 1] > kLazy;
@@ -752,9 +769,9 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       __syncwarp();  // this tile is in, and every lane has read the one before it
       fetch(stage == 0 ? kStages - 1 : stage - 1);
       const uint32_t at = ring + stage * Shape::kStageBytes;
-      if (key0 + kTile - 1 <= cur.s.L - p.Tq && (p.window < 0 || key0 >= cur.s.L - 1 - p.window))
+      if (key0 <= plain_to && (p.window < 0 || key0 >= cur.s.L - 1 - p.window))
         tile(at, at + 2 * Shape::kCodeBytes, key0, std::false_type(), std::integral_constant<int, kHalves>());
-      else  // some row does not see some key: rare in long caches, and kept small
+      else  // some row does not see some key, or a score has two factors: rare in long caches, and kept small
 #pragma unroll 1
         for (int y = 0; y < kHalves; ++y)
           tile(at + 16 * y * kRowBytes, at + 2 * Shape::kCodeBytes + 16 * y * kGroups * 4, key0 + 16 * y,

@@ -34,7 +34,7 @@ def test_huge_values(bits, group, size, Tk):
     decode_of(k, v, randn((2, 1, 4, 128), 3, 0.2), bits, group, [Tk, Tk // 2])
 
 
-@pytest.mark.parametrize("size", [2.0 ** 20, 1e10, 1e25, 1e35])
+@pytest.mark.parametrize("size", [2.0 ** 20, 1e10, 1e25, 1e35, 1e37])
 @pytest.mark.parametrize("Tk,Tq", [(20, 1), (700, 3), (6000, 1)])
 @pytest.mark.parametrize("bits,group", [(4, 64), (8, 32)])
 def test_huge_scores(bits, group, Tk, Tq, size):
@@ -69,3 +69,23 @@ def test_huge_scores(bits, group, Tk, Tq, size):
             size_of = (np.abs(values[b, h, keys]) + 2 * 2 ** bits * step[b, h, keys]).mean(0)
             tol = 2.0 ** -8 * np.abs(mean) + (2.0 ** -11 + 2.0 ** -14) * size_of
             assert (np.abs(cpu(o)[b, :, 3 * h:3 * h + 3] - mean) <= tol).all()
+
+
+@pytest.mark.parametrize("size_q,size_k,scale", [
+    (1e37, 2.0 ** -122, SCALE),               # the largest queries, the smallest keys
+    (1.0, 2.0 ** -112, 2.0 ** 112 * SCALE),   # the softmax scale in their place
+    (2.0 ** 60, 2.0 ** -122, 2.0 ** 62 * SCALE),
+    (2.0 ** 100, 2.0 ** -118, 2.0 ** 18 * SCALE),
+    (2.0 ** -118, 2.0 ** 100, 2.0 ** 18 * SCALE),
+    (2.0 ** -112, 1.0, 2.0 ** 112 * SCALE)])
+@pytest.mark.parametrize("bits,group", BITS_GROUPS)
+def test_queries_and_scales_of_any_size(bits, group, size_q, size_k, scale):
+    """Ordinary scores from queries, keys and a softmax scale whose sizes cancel. Every other head's query is smaller by
+    2^12, and one of them 0: their scores are small or 0, not lost to the others' range."""
+    B, Tq, H, Hkv, Tk = 2, 2, 8, 2, 300
+    q = randn((B, Tq, H, 128), 7, 0.2).double() * size_q
+    q[:, :, 1::2] *= 2.0 ** -12
+    q[:, :, 3] = 0
+    k = randn((B, Tk, Hkv, 128), 8, 0.2).double() * size_k
+    decode_of(k, randn((B, Tk, Hkv, 128), 9), q, bits, group, [Tk, 33], scale)
+    decode_of(k, randn((B, Tk, Hkv, 128), 9), q, bits, group, [Tk, 33], scale, window=40)
