@@ -58,6 +58,9 @@ constexpr int kKvqWarps = 12;     // warps per CTA (divides by 1, 2, 3 and 4 row
 constexpr int kKvqThreads = kKvqWarps * 32;
 constexpr int kKvqCtas = 148;     // CTAs of the split kernel, at most: one per SM of a 148-SM part
 
+// Running max of a row before its first key: fp32's lowest number, below which there is no score.
+constexpr float kKvqNone = -3.402823466e38f;
+
 // Places of a unit in the row beside its tiles: its queries, its first maximum and its result take a warp about as long
 // as two tiles do (one or none measured 3 and 20 % slower on decode_d20, whose batch holds short sequences).
 constexpr int kKvqUnitCost = 2;
@@ -321,8 +324,6 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   constexpr int kWords = kGroup * kBits / 128;   // 32-bit words of a key row and group that a lane scores
   constexpr int kVWords = kGroup * kBits / 256;  // of a value row and group that a lane multiplies (0: half a word)
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
-  constexpr float kNone = -3e38f;                // running max before the first key
-  constexpr float kMost = 3.402823466e38f;       // fp32's largest number
   constexpr int kLift = 120;
   // A score passes the running max by at most kLazy (log2) and |s| unit is at most kMostScale without a raise, so that
   // a weight is at most 2^15, in fp16's range.
@@ -554,14 +555,14 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       }
       const int e = 25 - up;  // in [-101, 139]
       float back = p.half_scale_log2 * kvq_power(min(e, 127)) * kvq_power(max(e - 127, 0));
-      if (back == INFINITY) back = -fminf(p.half_scale_log2 * kvq_power(-kLift / 2) * kvq_power(e - kLift / 2), kMost);
+      if (back == INFINITY) back = -fminf(p.half_scale_log2 * kvq_power(-kLift / 2) * kvq_power(e - kLift / 2), -kKvqNone);
       down[0] = __shfl_sync(0xffffffffu, back, 8 * t);
       down[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
     // the last tile that needs no mask begins here, if any (none where a score has two factors: those are the masked
     // tiles', so that the others do without; a flag of its own was 1 % slower)
     const int plain_to = __any_sync(0xffffffffu, down[0] < 0.f || down[1] < 0.f) ? -1 : cur.s.L - p.Tq - (kTile - 1);
-    float acc[8][4], corr[kGroups][2], m[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
+    float acc[8][4], corr[kGroups][2], m[2] = {kKvqNone, kKvqNone}, l[2] = {0.f, 0.f};
     float unit[kGroups][2];  // the weights p s of columns 2 t, 2 t + 1 are in units of 1 / unit, a power of two
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
@@ -854,7 +855,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
     for (; r < R; r += kKvqWarps) {
       auto slot_of = [&](int s) { return s ? 0 : i0 & 1; };
       auto warp_of = [&](int s) { return (i0 / 2 + s) * n_rt + r / 8; };  // piece s: its stretch's warp that had row r
-      float2 ml = make_float2(kNone, 0.f);
+      float2 ml = make_float2(kKvqNone, 0.f);
       if (lane < pieces) ml = *reinterpret_cast<const float2*>(piece_ml(slot_of(lane), warp_of(lane)) + (r % 8) * 2);
       float M = ml.x;
 #pragma unroll
@@ -918,7 +919,7 @@ __global__ void __launch_bounds__(256) kvq_decode_merge_kernel(const KvqDecodePa
   const int n = span.last_cta - x + 1;  // pieces: this CTA's slot, then the first slot of each CTA after it
   if (!ATTN_IN_RANGE(span.last_cta, 1, gridDim.x, kSiteKvqDecPart, &g_kvq_error)) return;
   const int r = blockIdx.y * kRows + warp / kSlices;
-  float M = -3e38f, l = 0.f;
+  float M = kKvqNone, l = 0.f;
   float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
   if (r < R) {
     constexpr int kAtOnce = 4;

@@ -89,3 +89,21 @@ def test_queries_and_scales_of_any_size(bits, group, size_q, size_k, scale):
     k = randn((B, Tk, Hkv, 128), 8, 0.2).double() * size_k
     decode_of(k, randn((B, Tk, Hkv, 128), 9), q, bits, group, [Tk, 33], scale)
     decode_of(k, randn((B, Tk, Hkv, 128), 9), q, bits, group, [Tk, 33], scale, window=40)
+
+
+@pytest.mark.parametrize("Tk", [5, 300, 6000])
+def test_the_lowest_scores(Tk):
+    """Every score -2.22e38 (in base 2 -3.203e38, fp32's end is -3.403e38): keys that are seen and weigh alike, so o is
+    the values' mean and lse the score."""
+    cache = attn.kvq_cache(1, 1, Tk, 8, 64)
+    v = randn((1, Tk, 1, 128), 5, 0.0)
+    attn.kvq_write(cache, torch.full((1, Tk, 1, 128), -2.609375 * 2.0 ** 59, dtype=torch.bfloat16, device="cuda"), v.cuda(),
+                   ints([Tk]))
+    q = torch.full((1, 1, 2, 128), 2.0 ** 60, dtype=torch.bfloat16, device="cuda")
+    o, lse = attn.attn_decode_kvq(q, cache, ints([Tk]), 1.0)
+    clean()
+    assert np.allclose(cpu(lse), -2.609375 * 2.0 ** 126, rtol=2.0 ** -20, atol=0)
+    step = cpu(cache.v_params[0, 0, :, :, 0]).repeat(64, -1)
+    values = cpu(cache.v_codes[0, 0]) * step + cpu(cache.v_params[0, 0, :, :, 1]).repeat(64, -1)
+    mean, size = values.mean(0), (np.abs(values) + 2 * 256 * step).mean(0)
+    assert (np.abs(cpu(o)[0, 0] - mean) <= 2.0 ** -8 * np.abs(mean) + (2.0 ** -11 + 2.0 ** -14) * size).all()
