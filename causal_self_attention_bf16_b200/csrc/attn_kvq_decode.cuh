@@ -826,9 +826,12 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   // Sequences without keys: o = 0, lse = -inf, shared out over the CTAs.
   for (int b = __any_sync(0xffffffffu, empty) ? blockIdx.x : p.B; b < p.B; b += gridDim.x) {
     if (kvq_seq<kTile>(p, b).tiles > 0) continue;
-    uint4* o4 = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(b) * p.Tq * p.H * 128);
-    for (int i = tid; i < p.Tq * p.H * 16; i += kKvqThreads) o4[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = tid; i < p.Tq * p.H; i += kKvqThreads) p.lse[static_cast<size_t>(b) * p.Tq * p.H + i] = -INFINITY;
+    const size_t rows = static_cast<size_t>(p.Tq) * p.H;  // (counted in 28 bits, their 16-byte parts are not)
+    for (size_t i = tid + b * rows * 16; i < (b + 1) * rows * 16; i += kKvqThreads)
+      if (ATTN_IN_RANGE(i * 8, 8, n_q, kSiteKvqDecO, &g_kvq_error))
+        reinterpret_cast<uint4*>(p.o)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (size_t i = tid + b * rows; i < (b + 1) * rows; i += kKvqThreads)
+      if (ATTN_IN_RANGE(i, 1, n_q / 128, kSiteKvqDecLse, &g_kvq_error)) p.lse[i] = -INFINITY;
   }
   cp_async_wait<0>();
   __syncthreads();

@@ -205,3 +205,23 @@ def test_debug_build_matches_release_on_the_quantised_cache(libs, bits, group, H
     assert _error_word(debug) == (0, 0), "an address check fired on valid inputs"
     for i, (a, b) in enumerate(zip(ref, got)):
         assert torch.equal(a, b), f"output {i} differs between the builds"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Tk", [(3, 40), (5, 901)])
+def test_debug_build_matches_release_on_quantised_sequences_without_keys(libs, B, Tk):
+    """Empty sequences before, between and after others, in whole units and split over CTAs."""
+    release, debug = libs
+    dev = torch.device("cuda:0")
+    g = torch.Generator().manual_seed(Tk)
+    H, Hkv, Tq, T = 6, 2, 2, 7
+    q, k, v = (_randn((B, n, h, 128), g, dev) for n, h in ((Tq, H), (T, Hkv), (T, Hkv)))
+    cache = attn.kvq_cache(B, Hkv, Tk, 4, 64, dev)
+    lens = torch.tensor([0, Tk, 0, 5, 0][:B], dtype=torch.int32, device=dev)
+    assert debug.attn_clear_device_error() == 0
+    ref = _kvq(release, q, k, v, cache, lens, 4, 64, -1)
+    got = _kvq(debug, q, k, v, cache, lens, 4, 64, -1)
+    assert _error_word(debug) == (0, 0), "an address check fired on valid inputs"
+    for i, (a, b) in enumerate(zip(ref, got)):
+        assert torch.equal(a, b), f"output {i} differs between the builds"
+    assert (got[-2][lens == 0] == 0).all() and (got[-1][lens == 0] == -float("inf")).all()

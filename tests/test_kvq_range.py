@@ -107,3 +107,19 @@ def test_the_lowest_scores(Tk):
     values = cpu(cache.v_codes[0, 0]) * step + cpu(cache.v_params[0, 0, :, :, 1]).repeat(64, -1)
     mean, size = values.mean(0), (np.abs(values) + 2 * 256 * step).mean(0)
     assert (np.abs(cpu(o)[0, 0] - mean) <= 2.0 ** -8 * np.abs(mean) + (2.0 ** -11 + 2.0 ** -14) * size).all()
+
+
+def test_a_sequence_without_keys_under_the_most_heads():
+    """2^27 query heads (o is 32 GiB, 2^31 parts of 16 bytes) over one empty sequence: every row is 0 and -inf."""
+    H, Hkv = 1 << 27, 1 << 22
+    if torch.cuda.mem_get_info()[0] < (70 << 30):
+        pytest.skip("not enough free device memory")
+    cache = attn.kvq_cache(1, Hkv, 1, 4, 128)
+    q = torch.empty(1, 1, H, 128, dtype=torch.bfloat16, device="cuda")
+    o = torch.full_like(q, float("nan"))
+    lse = torch.full((1, H, 1), float("nan"), device="cuda")
+    attn.attn_decode_kvq(q, cache, ints([0]), o=o, lse=lse)
+    clean()
+    assert all((part == 0).all() for part in o.view(64, -1)) and (lse == -float("inf")).all()
+    del cache, q, o, lse
+    torch.cuda.empty_cache()
