@@ -30,8 +30,10 @@
 //   that is lost). Per row, since a row must not lose its weights to the scale of a key that it does not see or
 //   hardly weighs (one unit for all rows was 0.5 % faster, 3 % in groups of 32). The second sum is fp32 throughout.
 //   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 4 (then p <= 2^4
-//   and the sums stay far from overflow) or a scale its unit by 2^11: one vote a tile in place of the reduction and
-//   the rescaling.
+//   and the sums stay far from overflow) or a weight times a scale its unit by 2^15: one vote a tile in place of the
+//   reduction and the rescaling. The vote takes a lane's largest weight times its largest scale. With the scales alone
+//   a heavy key without a value, whose unit the other keys' small weights set, made every tile after it raise (64
+//   sequences of 1,024 to 2,048 keys, 10 heads: 38.9 us against 35.5 at 4 bits, 52.0 against 44.3 in groups of 32).
 //
 // Work split. A unit is one (sequence, key/value head); its visible keys, tiles of 32 (8 bits: 16). All units' tiles
 // in a row, with two places more for each unit's own cost, are dealt to the warps in equal stretches, found on the
@@ -325,9 +327,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   constexpr int kVWords = kGroup * kBits / 256;  // of a value row and group that a lane multiplies (0: half a word)
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
   constexpr int kLift = 120;
-  // A score passes the running max by at most kLazy (log2) and |s| unit is at most kMostScale without a raise, so that
-  // a weight is at most 2^15, in fp16's range.
-  constexpr float kLazy = 4.f, kMostScale = 2048.f, kMostUnit = 0x1p100f;
+  // A weight is at most kLazy, and with its scale and unit kMostWeight, without a raise: in fp16's range.
+  constexpr float kLazy = 16.f, kMostWeight = 32768.f, kMostUnit = 0x1p100f;
   extern __shared__ __align__(128) uint8_t kvq_smem[];
   __shared__ KvqPiece sh_piece[2 * kKvqWarps];  // stretch i's slots at 2 i, 2 i + 1
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
@@ -628,8 +629,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       }
       // In log2 units a score is rounded before the max, one of them, comes off: the largest one then weighs 1 however
       // large it is. (An unrounded product less the max left it half a unit in the last place, 2^7 at 2^31.)
-      float x[4 * kN];  // log2 of the weights
-      bool raise = false;
+      float x[4 * kN], most_x[2] = {0.f, 0.f};  // the weights, and the lane's largest of each column
 #pragma unroll
       for (int e = 0; e < 4 * kN; e += 2) {
         F2 score = f2(s[e], s[e + 1]), factor = f2(down[0], down[1]);
@@ -640,9 +640,10 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         score = mul2(score, factor);
         const F2 less = add2(score, f2(-m[0], -m[1]));
         s[e] = lo_of(score), s[e + 1] = hi_of(score);
-        x[e] = seen[e] ? lo_of(less) : -INFINITY, x[e + 1] = seen[e + 1] ? hi_of(less) : -INFINITY;
-        raise |= x[e] > kLazy || x[e + 1] > kLazy;
+        x[e] = seen[e] ? ex2(lo_of(less)) : 0.f, x[e + 1] = seen[e + 1] ? ex2(hi_of(less)) : 0.f;
+        most_x[0] = fmaxf(most_x[0], x[e]), most_x[1] = fmaxf(most_x[1], x[e + 1]);
       }
+      bool raise = most_x[0] > kLazy || most_x[1] > kLazy;
       uint32_t vsz[2 * kN][kGroups];
 #pragma unroll
       for (int y = 0; y < 2 * kN; ++y) lds(vsz[y], ap + kp_lds + Shape::kParamBytes + 8 * y * kGroups * 4);
@@ -652,7 +653,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         top[j] = fabsf(__uint_as_float(vsz[0][j] << 16));
 #pragma unroll
         for (int y = 1; y < 2 * kN; ++y) top[j] = fmaxf(top[j], fabsf(__uint_as_float(vsz[y][j] << 16)));
-        raise |= top[j] * unit[j][0] > kMostScale || top[j] * unit[j][1] > kMostScale;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) raise |= most_x[c] * unit[j][c] * top[j] > kMostWeight;
       }
       if (__any_sync(0xffffffffu, raise)) {
         // A column's max becomes a whole number, so that the old weights' factor is a power of two, which their sums
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
           m[c] = y;
 #pragma unroll
           for (int e = c; e < 4 * kN; e += 2)
-            if (seen[e]) x[e] = s[e] - y;
+            if (seen[e]) x[e] = ex2(s[e] - y);
           l[c] *= f;
 #pragma unroll
           for (int j = 0; j < kGroups; ++j) corr[j][c] *= f;
@@ -683,8 +685,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
           for (int y = 0; y < 2 * kN; ++y) {
             const float sc = fabsf(__uint_as_float(vsz[y][j] << 16));
-            const float w0 = seen[2 * y] ? ex2(x[2 * y]) * sc : 0.f;
-            const float w1 = seen[2 * y + 1] ? ex2(x[2 * y + 1]) * sc : 0.f;
+            const float w0 = seen[2 * y] ? x[2 * y] * sc : 0.f;
+            const float w1 = seen[2 * y + 1] ? x[2 * y + 1] * sc : 0.f;
             most = __vmaxu2(most, __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632));
           }
 #pragma unroll
@@ -703,10 +705,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4 * kN; ++e) {
-        x[e] = ex2(x[e]);
-        l[e & 1] += x[e];
-      }
+      for (int e = 0; e < 4 * kN; ++e) l[e & 1] += x[e];
       // --- values
 #pragma unroll
       for (int y = 0; y < kN; ++y) {

@@ -123,3 +123,17 @@ def test_a_sequence_without_keys_under_the_most_heads():
     assert all((part == 0).all() for part in o.view(64, -1)) and (lse == -float("inf")).all()
     del cache, q, o, lse
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["null", "small", "often"])
+@pytest.mark.parametrize("bits,group", BITS_GROUPS)
+def test_a_heavy_key_of_little_value(bits, group, kind):
+    """A key that all rows weigh 2^12 to 2^20 times as much as any other, whose value is 0 (scale 0), or in steps 2^-12 of
+    the others' (once, or at every 61st key)."""
+    B, H, Hkv, Tk = 2, 4, 2, 3000
+    k = randn((B, Tk, Hkv, 128), 11, 0.0).float() * 0.1
+    v = randn((B, Tk, Hkv, 128), 12, 0.0).float()
+    at = slice(0, None, 61) if kind == "often" else 3
+    k[:, at] = 1.0
+    v[:, at] *= 0.0 if kind == "null" else 2.0 ** -12
+    decode_of(k, v, 1 + 0.1 * randn((B, 1, H, 128), 13, 0.0).float(), bits, group, [Tk, 2000])
