@@ -327,8 +327,11 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   constexpr int kVWords = kGroup * kBits / 256;  // of a value row and group that a lane multiplies (0: half a word)
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
   constexpr int kLift = 120;
-  // A weight is at most kLazy, and with its scale and unit kMostWeight, without a raise: in fp16's range.
-  constexpr float kLazy = 16.f, kMostWeight = 32768.f, kMostUnit = 0x1p100f;
+  // A weight is at most kLazy, and with its scale and unit kMostWeight, without a raise: in fp16's range. A unit is
+  // at most 2^kMostUnit, so that no product passes fp32's range before the scale comes to it; the weights of subnormal
+  // scales, down to 2^-133, are normal fp16 numbers still.
+  constexpr float kLazy = 16.f, kMostWeight = 32768.f;
+  constexpr int kMostUnit = 122;
   extern __shared__ __align__(128) uint8_t kvq_smem[];
   __shared__ KvqPiece sh_piece[2 * kKvqWarps];  // stretch i's slots at 2 i, 2 i + 1
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = 0.f, unit[j][0] = unit[j][1] = kMostUnit;
+    for (int j = 0; j < kGroups; ++j) corr[j][0] = corr[j][1] = 0.f, unit[j][0] = unit[j][1] = kvq_power(kMostUnit);
 
     // The tile of codes at `at` and params at `ap`: n_halves times 16 keys, from key0 on.
     auto tile = [&](const uint32_t at, const uint32_t ap, const int key0, auto masked, auto n_halves) {
@@ -696,7 +699,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
             // in exponent fields: the unit that the sums have now, and the one from here on, with which the largest
             // weight is below 2
             const int at = static_cast<int>(__float_as_uint(unit[j][c]) >> 23) + up[c];
-            const int to = max(min(min(at, 127 + 100), 2 * 127 - static_cast<int>((most >> (16 * c + 7)) & 0xffu)), 1);
+            const int aim = 2 * 127 - static_cast<int>((most >> (16 * c + 7)) & 0xffu);
+            const int to = max(min(min(at, 127 + kMostUnit), aim), 1);
             unit[j][c] = __uint_as_float(static_cast<uint32_t>(to) << 23);
             const float f = to - at < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + to - at) << 23);
 #pragma unroll

@@ -137,3 +137,13 @@ def test_a_heavy_key_of_little_value(bits, group, kind):
     k[:, at] = 1.0
     v[:, at] *= 0.0 if kind == "null" else 2.0 ** -12
     decode_of(k, v, 1 + 0.1 * randn((B, 1, H, 128), 13, 0.0).float(), bits, group, [Tk, 2000])
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -112, 2.0 ** -120])
+@pytest.mark.parametrize("Tk", [40, 3000])
+@pytest.mark.parametrize("bits,group", BITS_GROUPS)
+def test_tiny_values(bits, group, Tk, size):
+    """Values whose scales are near fp32's smallest normal number keep as many bits as others. (bf16 outputs below
+    2^-126 are rounded to 2^-134, which the weights' 2^-14 of 2 * 2^bits s covers.)"""
+    k, v = randn((2, Tk, 2, 128), 14, 0.2), randn((2, Tk, 2, 128), 15, 0.2).float() * size
+    decode_of(k, v, randn((2, 1, 4, 128), 16, 0.2), bits, group, [Tk, Tk // 3])
