@@ -26,8 +26,10 @@
 //   so that the fp32 accumulators hold sums of both signs: they are cut off, not rounded (1 + 1.5 * 2^-24 stays 1),
 //   which sums of one sign over a whole cache would show. p_j s_g is the B fragment, rounded to fp16: 2^-11 of itself
 //   at most against the output's own 2^-8. So that it is in fp16's range whatever the scales, it is carried in units
-//   of a power of two per query row and group of dims, in which the largest so far is 1 or more (one below 2^-25 of
-//   that is lost). Per row, since a row must not lose its weights to the scale of a key that it does not see or
+//   of a power of two per query row and group of dims, in which the largest so far is 2^8 or more: light keys behind a
+//   heavy one keep 2^-11 of themselves down to 2^-22 of it, and are lost below 2^-33 only. (The matrix unit cuts each
+//   product off at about 2^-24 of the sum it joins, so that this much counts where the heavy key's code is near the
+//   middle.) Per row, since a row must not lose its weights to the scale of a key that it does not see or
 //   hardly weighs (one unit for all rows was 0.5 % faster, 3 % in groups of 32). The second sum is fp32 throughout.
 //   Softmax in base 2 and fp32. The running max is only raised when a score passes it by more than 4 (then p <= 2^4
 //   and the sums stay far from overflow) or a weight times a scale its unit by 2^15: one vote a tile in place of the
@@ -327,11 +329,12 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
   constexpr int kVWords = kGroup * kBits / 256;  // of a value row and group that a lane multiplies (0: half a word)
   constexpr float kCentre = kBits == 4 ? 8.f : 128.f;
   constexpr int kLift = 120;
-  // A weight is at most kLazy, and with its scale and unit kMostWeight, without a raise: in fp16's range. A unit is
-  // at most 2^kMostUnit, so that no product passes fp32's range before the scale comes to it; the weights of subnormal
-  // scales, down to 2^-133, are normal fp16 numbers still.
+  // A weight is at most kLazy, and with its scale and unit kMostWeight, without a raise: in fp16's range. A raise puts
+  // a tile's largest into [2^kAim, 2^(kAim + 1)): near the range's upper end, with room for 2^6 before the next raise.
+  // A unit is at most 2^kMostUnit, so that no product passes fp32's range before the scale comes to it; the weights of
+  // subnormal scales, down to 2^-133, are normal fp16 numbers still.
   constexpr float kLazy = 16.f, kMostWeight = 32768.f;
-  constexpr int kMostUnit = 122;
+  constexpr int kAim = 8, kMostUnit = 122;
   extern __shared__ __align__(128) uint8_t kvq_smem[];
   __shared__ KvqPiece sh_piece[2 * kKvqWarps];  // stretch i's slots at 2 i, 2 i + 1
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
@@ -696,11 +699,10 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
           for (int o = 4; o < 32; o <<= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, o));
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            // in exponent fields: the unit that the sums have now, and the one from here on, with which the largest
-            // weight is below 2
+            // in exponent fields: the unit that the sums have now, and the one from here on
             const int at = static_cast<int>(__float_as_uint(unit[j][c]) >> 23) + up[c];
-            const int aim = 2 * 127 - static_cast<int>((most >> (16 * c + 7)) & 0xffu);
-            const int to = max(min(min(at, 127 + kMostUnit), aim), 1);
+            const int aim = 2 * 127 + kAim - static_cast<int>((most >> (16 * c + 7)) & 0xffu);
+            const int to = min(min(at, 127 + kMostUnit), aim);
             unit[j][c] = __uint_as_float(static_cast<uint32_t>(to) << 23);
             const float f = to - at < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + to - at) << 23);
 #pragma unroll

@@ -147,3 +147,38 @@ def test_tiny_values(bits, group, Tk, size):
     2^-126 are rounded to 2^-134, which the weights' 2^-14 of 2 * 2^bits s covers.)"""
     k, v = randn((2, Tk, 2, 128), 14, 0.2), randn((2, Tk, 2, 128), 15, 0.2).float() * size
     decode_of(k, v, randn((2, 1, 4, 128), 16, 0.2), bits, group, [Tk, Tk // 3])
+
+
+@pytest.mark.parametrize("heavy_code,z", [("middle", -1.546875), ("lowest", -1.1015625)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_many_light_keys_behind_a_heavy_one(bits, heavy_code, z):
+    """A key with most of the weight and 2^17 - 1 keys behind it, of 2^-25.2 or 2^-18 of it each, in one warp's stretch
+    (32 rows to a head: 148 x 3 stretches for as many units). The heavy key's value is 0, so they are all of the output.
+    A weight is rounded to 2^-11 of itself or 2^-33 of the heaviest and multiplies at most 2^(bits - 1) steps of its
+    scale. In each of 8192 matrix products the 16 products and the sum so far, at most the heavy key's code less the
+    middle one and all of the light keys' together, are cut off at 2^-23 of the largest. The fp32 sums of the weights,
+    and of the weights times the values' middle, take 2^14 terms a lane, each rounded by 2^-24 of the sum. o is bf16."""
+    Hkv, Tk, scale, middle = 148 * 3, 1 << 17, 128 ** -0.5, 2 ** (bits - 1)
+    if torch.cuda.mem_get_info()[0] < 2.5 * Hkv * Tk * (32 * bits + 8):
+        pytest.skip("not enough free device memory")
+    cache = attn.kvq_cache(1, Hkv, Tk, bits, 128)
+    code = middle if heavy_code == "middle" else 0
+    cache.v_codes.fill_(255)
+    cache.v_codes[:, :, 0] = 17 * code if bits == 4 else code
+    cache.v_params[..., 0] = 1
+    cache.v_params[..., 1] = -code
+    cache.k_params[..., 1] = z
+    cache.k_params[:, :, 0] = 0
+    q = torch.ones(1, 1, 32 * Hkv, 128, dtype=torch.bfloat16, device="cuda")
+    o, lse = attn.attn_decode_kvq(q, cache, ints([Tk]), scale)
+    clean()
+    light = (Tk - 1) * np.exp(z * 128 * np.float64(np.float32(scale)))
+    top, total = 2 ** bits - 1, 1 + light
+    want = (top - code) * light / total
+    sums = max(middle - code, middle * light)
+    tol = (2.0 ** -11 * light + 2.0 ** -33 * Tk) * middle + 17 * 8192 * 2.0 ** -23 * sums
+    tol += 2.0 ** -10 * ((middle - code) * total + want)
+    assert np.abs(cpu(lse) - np.log(total)).max() <= 2.0 ** -10
+    assert np.abs(cpu(o) - want).max() <= 2.0 ** -8 * want + tol / total, (np.abs(cpu(o) - want).max(), tol, want)
+    del cache
+    torch.cuda.empty_cache()
