@@ -710,8 +710,10 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
           }
         }
       }
+      F2 sum = f2(x[0], x[1]);  // (the tile's by themselves first: a light key may be lost to what a heavy one left)
 #pragma unroll
-      for (int e = 0; e < 4 * kN; ++e) l[e & 1] += x[e];
+      for (int e = 2; e < 4 * kN; e += 2) sum = add2(sum, f2(x[e], x[e + 1]));
+      l[0] += lo_of(sum), l[1] += hi_of(sum);
       // --- values
 #pragma unroll
       for (int y = 0; y < kN; ++y) {

@@ -156,8 +156,9 @@ def test_many_light_keys_behind_a_heavy_one(bits, heavy_code, z):
     (32 rows to a head: 148 x 3 stretches for as many units). The heavy key's value is 0, so they are all of the output.
     A weight is rounded to 2^-11 of itself or 2^-33 of the heaviest and multiplies at most 2^(bits - 1) steps of its
     scale. In each of 8192 matrix products the 16 products and the sum so far, at most the heavy key's code less the
-    middle one and all of the light keys' together, are cut off at 2^-23 of the largest. The fp32 sums of the weights,
-    and of the weights times the values' middle, take 2^14 terms a lane, each rounded by 2^-24 of the sum. o is bf16."""
+    middle one and all of the light keys' together, are cut off at 2^-23 of the largest. The fp32 sums of the weights
+    times the values' middle take 2^14 terms a lane, each rounded by 2^-24 of the sum; the sums of the weights 2^13 (8
+    bits) or 2^12 tiles' sums. o is bf16."""
     Hkv, Tk, scale, middle = 148 * 3, 1 << 17, 128 ** -0.5, 2 ** (bits - 1)
     if torch.cuda.mem_get_info()[0] < 2.5 * Hkv * Tk * (32 * bits + 8):
         pytest.skip("not enough free device memory")
@@ -178,7 +179,7 @@ def test_many_light_keys_behind_a_heavy_one(bits, heavy_code, z):
     sums = max(middle - code, middle * light)
     tol = (2.0 ** -11 * light + 2.0 ** -33 * Tk) * middle + 17 * 8192 * 2.0 ** -23 * sums
     tol += 2.0 ** -10 * ((middle - code) * total + want)
-    assert np.abs(cpu(lse) - np.log(total)).max() <= 2.0 ** -10
+    assert np.abs(cpu(lse) - np.log(total)).max() <= 2.0 ** -11 + 2.0 ** -20
     assert np.abs(cpu(o) - want).max() <= 2.0 ** -8 * want + tol / total, (np.abs(cpu(o) - want).max(), tol, want)
     del cache
     torch.cuda.empty_cache()
