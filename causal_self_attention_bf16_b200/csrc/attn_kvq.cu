@@ -36,20 +36,20 @@ namespace {
 
 using attn::g_cuda_error;
 
-// Threads per block: 256 made write 3 % slower (its registers leave no whole number of such blocks on an SM), 128 made
-// read 12 to 38 % slower.
+// Threads per block: 256 made write 3 to 5 % slower (its registers leave no whole number of such blocks on an SM), 128
+// made read 9 to 36 % slower.
 constexpr int kReadThreads = 256, kWriteThreads = 128;
 constexpr int kReadLanes = 16, kWriteLanes = 8;  // threads per row
 // Blocks of write, at most: six times the nine that an SM holds. Blocks with one set of rows each were slower in
-// batches of padded prompts, where many have nothing to do (32 prompts of up to 2,048 tokens: 56 us against 49), and a
-// single wave of them in full ones (104 us against 86).
+// batches of padded prompts, where many have nothing to do (32 prompts of up to 2,048 tokens, 10 heads, 4 bits in
+// groups of 32: 51 us against 47), and a single wave of them in full ones (102 us against 86).
 constexpr unsigned kWriteBlocks = 148 * 54;
 enum : uint32_t {
   kSiteKvqNew = 0xa0, kSiteKvqCodes = 0xa1, kSiteKvqParams = 0xa2, kSiteKvqOut = 0xa3
 };
 
 // Division by a number known on the host: n / d for n < 2^31 (the high half of n times 2^32 (2^shift / d - 1), rounded
-// up, plus n, shifted).
+// up, plus n, shifted: Granlund and Montgomery, "Division by invariant integers using multiplication", 1994).
 struct FastDiv {
   uint32_t d, mul, shift;
   FastDiv(uint32_t d_ = 1) : d(d_), mul(0), shift(0) {
@@ -112,8 +112,8 @@ __device__ __forceinline__ void quantise16(const uint32_t (&w)[8], uint32_t (&co
   const float span = __bfloat162float(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx))) - z;
   // Quotients by Markstein's method (IBM J. Res. Dev. 34, 1990): with y = 1 / b rounded to nearest and q = a y, the
   // sum q + (a - q b) y, the remainder exact, is a / b rounded to nearest. Nothing less will do: bf16 numbers over a
-  // bf16 scale lie on ties often (one in 50 at 4 bits). The compiler's divisions took 2.8 times as long (234 us
-  // against 83 for 32 x 2048 tokens of 10 heads at 4 bits, groups of 32). Added to 1.5 * 2^23 a quotient is rounded
+  // bf16 scale lie on ties often (one in 50 at 4 bits). The compiler's divisions took 2.6 times as long (226 us
+  // against 86 for 32 x 2048 tokens of 10 heads at 4 bits, groups of 32). Added to 1.5 * 2^23 a quotient is rounded
   // to an integer in the sum's low bits.
   constexpr float kMagic = 12582912.f, kInverse = 1.f / kLevels;
   uint32_t t[16];
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(kWriteThreads) kvq_write_kernel(const CopyPara
     const uint32_t r = r0 + threadIdx.x / kWriteLanes;
     const bool live = r < rows;  // (every lane stays for the shuffles)
     const CopyRow at = copy_row(p, live ? r : 0u);
-    // A warp whose tokens have no position reads nothing: half of a batch of left-padded prompts may be such (59 us
-    // against 81 for 32 prompts of up to 2,048 tokens; with none of them loads that wait for the lengths cost 4 %).
+    // A warp whose tokens have no position reads nothing: half of a batch of left-padded prompts may be such (47 us
+    // against 80 for 32 prompts of up to 2,048 tokens; with none of them loads that wait for the lengths cost 1 to 4 %).
     if (!__any_sync(0xffffffffu, live && at.there)) continue;
     const size_t from = at.dense * size_t{128} + 16 * c;
     const bool in = ATTN_IN_RANGE(from, 16, n_new, kSiteKvqNew, &g_kvq_error);

@@ -7,8 +7,9 @@
 // lane), so the codes go to the matrix unit, as A fragments of mma.m16n8k16 (fp16 in, fp32 sums) made in registers.
 // tcgen05 would need them widened in shared or tensor memory first, four bytes written for every byte read, to fill
 // 128-row tiles with 1 to 32 queries. What bounds the loop at 4 bits is the memory and the widening together, so that
-// is kept to few operations. 256 sequences of 1,024 to 2,048 keys with 10 heads, groups of 64: 107 us, 5.3 TB/s (81 %
-// of the copy); 95 us with the arithmetic taken out. Long runs meet the power cap, 122 us at 1.73 GHz.
+// is kept to few operations. 256 sequences of 1,024 to 2,048 keys with 10 heads, groups of 64: 112 us, 5.1 TB/s (77 %
+// of the copy) in a graph of a few calls; 95 us with the arithmetic taken out. A loop of calls meets the power cap: 117
+// to 125 us.
 //
 //   Codes. A small integer in the low bits of an fp16 number is that number: n * 2^-24, a subnormal, which the matrix
 //   unit multiplies exactly. So one logical operation makes two numbers of a 32-bit word's low nibbles (n * 2^-24), of
@@ -319,7 +320,7 @@ __device__ __forceinline__ void kvq_next_unit(const KvqDecodeParams& p, KvqCurso
 
 // A warp takes up to 8 query rows; with more, n_rt = ceil(R / 8) warps take a stretch's tiles together, each for itself
 // (32 rows: 24 us where the bytes would take 2.3). 12 warps of 168 registers an SM: 16 of 128 took half as many
-// instructions again.
+// instructions again. Groups of 32 dims do not quite fit: at 4 bits some 170 bytes a thread are spilled, at 8 bits 8.
 template <int kBits, int kGroup>
 __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const KvqDecodeParams p) {
   using Shape = KvqShape<kBits, kGroup>;
@@ -562,7 +563,8 @@ __global__ void __launch_bounds__(kKvqThreads, 1) kvq_decode_split_kernel(const 
       }
       const int e = 25 - up;  // in [-101, 139]
       float back = p.half_scale_log2 * kvq_power(min(e, 127)) * kvq_power(max(e - 127, 0));
-      if (back == INFINITY) back = -fminf(p.half_scale_log2 * kvq_power(-kLift / 2) * kvq_power(e - kLift / 2), -kKvqNone);
+      if (back == INFINITY)
+        back = -fminf(p.half_scale_log2 * kvq_power(-kLift / 2) * kvq_power(e - kLift / 2), -kKvqNone);
       down[0] = __shfl_sync(0xffffffffu, back, 8 * t);
       down[1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }

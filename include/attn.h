@@ -277,7 +277,7 @@ attn_status attn_kvq_read(const void* k_codes, const void* k_params, const void*
  * codes stand for (not rounded to bf16 in between). Forward only. A query's dims count to 2^-35 of its largest. A
  * key's weight times its value's scale is rounded to fp16, 2^-11 of itself (against o's own 2^-8), or to 2^-33 of the
  * largest of that query and group so far, or to 2^-147; scores, weights and sums are fp32, but the sums of weights times
- * codes are cut off, not rounded: a key's part counts to about 2^-24 of the sum so far.
+ * codes are cut off, not rounded: a key's part counts to about 2^-24 of the sum so far. A weight below 2^-126 is 0.
  * Queries, keys and scale may be of any size whose scores fp32 holds, while scale times a query's largest dim is below
  * 2^230. The sums over keys are fp32 and divided by the weights' sum at the end, so the values' sum with weights of
  * about 1 for a row's largest key (2^4 at most) has to stay below 2^128.

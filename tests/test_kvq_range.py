@@ -59,7 +59,9 @@ def test_huge_scores(bits, group, Tk, Tq, size):
     clean()
     top = 15 * np.float64(np.float32(0.0883)) * cpu(q)[..., 0].transpose(0, 2, 1)
     assert (np.abs(cpu(lse) - top - np.log(3)) <= 2.0 ** -20 * top + 2.0 ** -20).all()
-    codes = (cache.v_codes[..., None] >> torch.tensor([0, 4], device="cuda") & 15).flatten(-2) if bits == 4 else cache.v_codes
+    codes = cache.v_codes
+    if bits == 4:
+        codes = (codes[..., None] >> torch.tensor([0, 4], device="cuda") & 15).flatten(-2)
     step = cpu(cache.v_params[..., 0].repeat_interleave(group, -1))
     values = cpu(codes) * step + cpu(cache.v_params[..., 1].repeat_interleave(group, -1))
     for b in range(B):
@@ -97,8 +99,8 @@ def test_the_lowest_scores(Tk):
     the values' mean and lse the score."""
     cache = attn.kvq_cache(1, 1, Tk, 8, 64)
     v = randn((1, Tk, 1, 128), 5, 0.0)
-    attn.kvq_write(cache, torch.full((1, Tk, 1, 128), -2.609375 * 2.0 ** 59, dtype=torch.bfloat16, device="cuda"), v.cuda(),
-                   ints([Tk]))
+    k = torch.full((1, Tk, 1, 128), -2.609375 * 2.0 ** 59, dtype=torch.bfloat16, device="cuda")
+    attn.kvq_write(cache, k, v.cuda(), ints([Tk]))
     q = torch.full((1, 1, 2, 128), 2.0 ** 60, dtype=torch.bfloat16, device="cuda")
     o, lse = attn.attn_decode_kvq(q, cache, ints([Tk]), 1.0)
     clean()
